@@ -80,6 +80,8 @@ typedef enum pkv_status {
 #define PKV_DEVERR_BLOCK_RANGE 0x2u  /* a block table entry outside [0, num_blocks) */
 #define PKV_DEVERR_LEN_RANGE 0x4u    /* a context/sequence length outside its stated bound */
 #define PKV_DEVERR_WAIT_TIMEOUT 0x8u /* a bounded pipeline wait gave up */
+#define PKV_DEVERR_NO_BLOCKS 0x10u   /* fork: no free block left for a child */
+#define PKV_DEVERR_REF_COUNT 0x20u   /* free: a block that nothing holds */
 
 /* Human-readable name of a status code.  Never NULL. */
 PKV_API const char* pkv_status_string(int status);
@@ -353,6 +355,238 @@ PKV_API pkv_status pkv_sample_exponential_race(const float* logits, int64_t row_
                                         int32_t batch, int32_t vocab, uint64_t seed, uint64_t offset,
                                         int32_t* out_tokens, void* workspace, size_t workspace_bytes,
                                         void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The 4-bit cache.
+ *
+ * Same blocks, slots and tables as the bf16 cache; a token row of one kv head
+ * (128 dims) is held as eight groups of 16 consecutive dims, each with one
+ * scale s (e4m3) and 16 codes (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives), so a row takes 72 bytes where bf16 takes 256.  Dim d stands for
+ *   code_d * s_group(d) * tensor_scale,
+ * with one tensor scale for K and one for V (1 unless a calibration says
+ * otherwise).  Storing x:
+ *   y = x * (1 / tensor_scale)   (fp32, the reciprocal rounded to fp32)
+ *   s = e4m3(min(max|y| / 6, 448)), code = e2m1(y / s)   (fp32 quotients)
+ * both rounded to nearest, ties to even, codes saturating at 6; a group whose
+ * s is zero (max|y| <= 6 * 2^-10) holds zeros, an infinity is held as
+ * 6 * 448 * tensor_scale with its sign, and a NaN makes its group of 16 read as
+ * NaN.
+ *
+ *   k_data, v_data      (num_blocks, block_size, num_kv_heads, 64) bytes: dim
+ *                       2i in the low nibble of byte i, dim 2i + 1 in the high
+ *                       one.
+ *   k_scales, v_scales  (num_blocks, block_size, num_kv_heads, 8) bytes (e4m3).
+ *   k_scale, v_scale    tensor scales, finite and > 0.
+ * All four arrays C-contiguous and 16-byte aligned; shapes as for the bf16
+ * cache.  The struct itself is read on the host during the call.
+ */
+typedef struct pkv_q4_cache {
+  uint8_t* k_data;
+  uint8_t* k_scales;
+  uint8_t* v_data;
+  uint8_t* v_scales;
+  float k_scale;
+  float v_scale;
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+} pkv_q4_cache;
+
+/*
+ * pkv_kv_cache_write into the 4-bit cache: arguments and slots as there.
+ */
+PKV_API pkv_status pkv_kv_cache_write_q4(const pkv_bf16* k, int64_t k_token_stride, const pkv_bf16* v,
+                                         int64_t v_token_stride, const int32_t* slot_mapping, int32_t num_tokens,
+                                         const pkv_q4_cache* cache, void* stream);
+
+/*
+ * Rows of a 4-bit cache back as bf16 (to move sequences to a bf16 cache or to
+ * another process): row i of k_out and v_out, [num_tokens, num_kv_heads,
+ * head_dim] contiguous, receives slot slots[i], the product
+ * code * s * tensor_scale rounded once.  Slot -1 gives zeros; a slot outside
+ * the cache gives zeros and flags PKV_DEVERR_SLOT_RANGE.
+ */
+PKV_API pkv_status pkv_kv_cache_read_q4(const pkv_q4_cache* cache, const int32_t* slots, int32_t num_tokens,
+                                        pkv_bf16* k_out, pkv_bf16* v_out, void* stream);
+
+/*
+ * Decode attention over the 4-bit cache: pkv_paged_attn_decode with K and V
+ * the values the cache holds.  Pad rows, bounds and the workspace's rules as
+ * there; the contents of slots at or behind a sequence's length do not matter
+ * (any bytes).  The values and the probabilities enter the products in fp16:
+ * code * s is exact there, and a query row is scaled by a power of two so that
+ * its largest element is in range, which loses nothing of elements down to
+ * 2^-29 of it.  Accumulation is fp32.
+ */
+PKV_API size_t pkv_decode_q4_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads);
+PKV_API pkv_status pkv_paged_attn_decode_q4(const pkv_bf16* q, const pkv_q4_cache* cache,
+                                            const int32_t* context_lens, const int32_t* block_tables,
+                                            int32_t max_blocks_per_seq, int32_t batch, int32_t num_q_heads,
+                                            int32_t max_context_len, float scale, pkv_bf16* out, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
+/*
+ * Varlen causal prefill over the 4-bit cache: pkv_paged_attn_prefill with K and
+ * V the values the cache holds; rounding as in pkv_paged_attn_decode_q4.
+ *   max_seqlen_q, max_seqlen_k  upper bounds of n_i and L_i.  A sequence beyond
+ *                 them, with c_i < 0 or with L_i > max_blocks_per_seq *
+ *                 block_size flags PKV_DEVERR_LEN_RANGE and its rows are not
+ *                 written.
+ *   workspace     >= pkv_prefill_q4_workspace_bytes(total_q, num_seqs,
+ *                 max_seqlen_q, max_seqlen_k, num_q_heads, num_kv_heads) device
+ *                 bytes, 256-byte aligned, need not be initialised.  When the
+ *                 query tiles are too few to occupy the GPU, the keys are split
+ *                 over several CTAs and the pieces joined from there.  The size
+ *                 depends on the current device's SM count.
+ */
+PKV_API size_t pkv_prefill_q4_workspace_bytes(int32_t total_q, int32_t num_seqs, int32_t max_seqlen_q,
+                                              int32_t max_seqlen_k, int32_t num_q_heads, int32_t num_kv_heads);
+PKV_API pkv_status pkv_paged_attn_prefill_q4(const pkv_bf16* q, const pkv_q4_cache* cache,
+                                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                             int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q,
+                                             int32_t max_seqlen_k, int32_t num_q_heads, float scale, pkv_bf16* out,
+                                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Norm and rotation of queries and keys (the Qwen3 attention layer's step
+ * between the fused projection and the cache).
+ *
+ * For every head row x of 128 dims, in fp32 with one rounding to bf16:
+ *   y_d = x_d * rsqrt(mean(x^2) + eps) * weight_d
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t)
+ * for the pairs (i, i + rope_dim/2) of the first rope_dim dims, or (2i, 2i + 1)
+ * when `interleaved`; the dims behind rope_dim are only normalised.
+ *
+ *   q_weight, k_weight  [128] bf16, 16-byte aligned; NULL leaves those rows
+ *                 unnormalised.
+ *   eps           >= 0.
+ *   freqs         [rope_dim/2] int64: the rotation per position of pair i as a
+ *                 fraction of a turn in units of 2^-64 (modulo one turn), so
+ *                 t = 2 pi * frac(position * freqs[i] / 2^64), exact for every
+ *                 int32 position.  For the usual base b: freqs[i] =
+ *                 round(b^(-2i/rope_dim) / (2 pi) * 2^64).
+ *   rope_dim      0, 32, 64, 96 or 128 (0: no rotation, freqs and positions
+ *                 may be NULL).
+ *   positions     position a of token i at element a * position_axis_stride + i
+ *                 (stride >= 0; 0: the same positions on every axis).
+ *   num_axes, sections  1 to 3 position axes (time, height, width); pairs
+ *                 0 .. sections[0]-1 follow axis 0, the next sections[1] axis 1,
+ *                 the rest axis 2.  The first num_axes sections add up to
+ *                 rope_dim/2 (with rope_dim 0 both are ignored).
+ * The struct is read on the host during the call.
+ */
+typedef struct pkv_norm_rope {
+  const pkv_bf16* q_weight;
+  const pkv_bf16* k_weight;
+  const int64_t* freqs;
+  const int32_t* positions;
+  int64_t position_axis_stride;
+  float eps;
+  int32_t rope_dim;
+  int32_t interleaved;
+  int32_t num_axes;
+  int32_t sections[3];
+} pkv_norm_rope;
+
+/*
+ * Queries and keys normalised and rotated.
+ *   q [num_tokens, num_q_heads, head_dim], k [num_tokens, num_kv_heads, head_dim]
+ *   bf16 with token strides (elements, multiples of 8; rows 16-byte aligned);
+ *   q_out, k_out likewise and they may be q and k themselves (same pointer and
+ *   stride) but must not overlap them otherwise.  num_kv_heads may be 0 (k and
+ *   k_out NULL) to treat queries alone.
+ */
+PKV_API pkv_status pkv_qk_norm_rope(const pkv_bf16* q, int64_t q_token_stride, const pkv_bf16* k,
+                                    int64_t k_token_stride, int32_t num_tokens, int32_t num_q_heads,
+                                    int32_t num_kv_heads, int32_t head_dim, const pkv_norm_rope* nr, pkv_bf16* q_out,
+                                    int64_t q_out_stride, pkv_bf16* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * The same with the step's K and V written into the cache in the same pass: the
+ * result of pkv_qk_norm_rope followed by pkv_kv_cache_write (or _write_q4) of
+ * its k_out and of v.  Rows of slot -1 write no K or V but their q_out.
+ */
+PKV_API pkv_status pkv_qk_norm_rope_write(const pkv_bf16* q, int64_t q_token_stride, const pkv_bf16* k,
+                                          int64_t k_token_stride, const pkv_bf16* v, int64_t v_token_stride,
+                                          int32_t num_tokens, int32_t num_q_heads, const pkv_norm_rope* nr,
+                                          const int32_t* slot_mapping, pkv_bf16* k_cache, pkv_bf16* v_cache,
+                                          int32_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                                          int32_t head_dim, pkv_bf16* q_out, int64_t q_out_stride, void* stream);
+PKV_API pkv_status pkv_qk_norm_rope_write_q4(const pkv_bf16* q, int64_t q_token_stride, const pkv_bf16* k,
+                                             int64_t k_token_stride, const pkv_bf16* v, int64_t v_token_stride,
+                                             int32_t num_tokens, int32_t num_q_heads, const pkv_norm_rope* nr,
+                                             const int32_t* slot_mapping, const pkv_q4_cache* cache, pkv_bf16* q_out,
+                                             int64_t q_out_stride, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Blocks of a cache.  ref_count [num_blocks] int32 says how many sequences hold
+ * a block (0: free); a sequence of length L holds the first ceil(L / 256)
+ * entries of its block table row.
+ *
+ * Fork: child i is a copy of sequence parents[i].  It shares the parent's full
+ * blocks (their counts rise by one); if its last block is partly filled, the
+ * child gets a free block for it, the i-th child that needs one the i-th
+ * smallest free id, and copy_src[i] -> copy_dst[i] is the block to copy (-1, -1
+ * for the others; hand both lists to pkv_copy_blocks).
+ *   child_tables  [num_forks, max_blocks_per_seq] (-1 behind the blocks),
+ *   child_lens, copy_src, copy_dst  [num_forks]; none may overlap the inputs.
+ * A parent outside [0, num_seqs) or with a length out of bounds flags
+ * PKV_DEVERR_LEN_RANGE, one with a block out of range or with count 0 flags
+ * PKV_DEVERR_BLOCK_RANGE, and a child for which no block is left flags
+ * PKV_DEVERR_NO_BLOCKS: such a child is empty (length 0) and holds nothing.
+ * num_forks <= 8192.
+ */
+PKV_API pkv_status pkv_fork_blocks(const int32_t* block_tables, const int32_t* context_lens, int32_t num_seqs,
+                                   int32_t max_blocks_per_seq, const int32_t* parents, int32_t num_forks,
+                                   int32_t* ref_count, int32_t num_blocks, int32_t* child_tables,
+                                   int32_t* child_lens, int32_t* copy_src, int32_t* copy_dst, void* stream);
+
+/*
+ * Free: every block held by the num_seqs rows given loses one reference.  The
+ * rows themselves are left as they are.  A length out of bounds flags
+ * PKV_DEVERR_LEN_RANGE (the row is skipped), an id out of range
+ * PKV_DEVERR_BLOCK_RANGE, and a block whose count is used up
+ * PKV_DEVERR_REF_COUNT (its count stays 0).
+ */
+PKV_API pkv_status pkv_free_blocks(const int32_t* block_tables, const int32_t* context_lens, int32_t num_seqs,
+                                   int32_t max_blocks_per_seq, int32_t* ref_count, int32_t num_blocks, void* stream);
+
+/*
+ * Compact: with n blocks of count > 0, the i-th smallest such id >= n moves to
+ * the i-th smallest other id < n, so that the live blocks become 0 .. n-1.
+ *   copy_src, copy_dst  [num_blocks / 2]: the moves, -1 behind them (hand both
+ *                 to pkv_copy_blocks); num_moves [1] their number.
+ *   new_tables    [num_seqs, max_blocks_per_seq]: block_tables with the ids of
+ *                 moved blocks replaced in the entries that sequences hold;
+ *                 every other entry unchanged.
+ *   new_ref_count [num_blocks].
+ * new_tables may be block_tables and new_ref_count may be ref_count.  Entries
+ * out of range or of blocks that nothing holds flag PKV_DEVERR_BLOCK_RANGE and
+ * stay; rows with a length out of bounds flag PKV_DEVERR_LEN_RANGE and stay.
+ */
+PKV_API pkv_status pkv_compact_blocks(const int32_t* block_tables, const int32_t* context_lens, int32_t num_seqs,
+                                      int32_t max_blocks_per_seq, const int32_t* ref_count, int32_t num_blocks,
+                                      int32_t* new_tables, int32_t* new_ref_count, int32_t* copy_src,
+                                      int32_t* copy_dst, int32_t* num_moves, void* stream);
+
+/*
+ * Copy blocks src[i] -> dst[i], i < num_copies, in every plane of a cache: plane
+ * p (a layer's K or V, or its codes or scales) holds num_blocks blocks of
+ * block_bytes from byte p * plane_stride_bytes of `cache` on.  Pairs of -1 are
+ * skipped, pairs with an id out of range are skipped and flag
+ * PKV_DEVERR_BLOCK_RANGE.  The destinations must be distinct and none of them a
+ * source of another pair (what they receive is unspecified otherwise).
+ * block_bytes, plane_stride_bytes and the address are multiples of 16.
+ */
+PKV_API pkv_status pkv_copy_blocks(void* cache, int32_t num_planes, int64_t plane_stride_bytes, int32_t num_blocks,
+                                   int64_t block_bytes, const int32_t* src, const int32_t* dst, int32_t num_copies,
+                                   void* stream);
 
 /*
  * Read (and, if `clear` is nonzero, reset) the device error word of the

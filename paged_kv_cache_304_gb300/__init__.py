@@ -29,7 +29,8 @@ STATUS = {
     0: "PKV_OK", -1: "PKV_ERR_NULL", -2: "PKV_ERR_SHAPE", -3: "PKV_ERR_UNSUPPORTED",
     -4: "PKV_ERR_WORKSPACE", -5: "PKV_ERR_CUDA", -6: "PKV_ERR_ALIGN",
 }
-DEVERR = {0x1: "SLOT_RANGE", 0x2: "BLOCK_RANGE", 0x4: "LEN_RANGE", 0x8: "WAIT_TIMEOUT"}
+DEVERR = {0x1: "SLOT_RANGE", 0x2: "BLOCK_RANGE", 0x4: "LEN_RANGE", 0x8: "WAIT_TIMEOUT", 0x10: "NO_BLOCKS",
+          0x20: "REF_COUNT"}
 
 _lock = threading.Lock()
 _lib = None
@@ -97,6 +98,26 @@ def load(path: str | None = None):
         lib.pkv_paged_attn_prefill_fused_write.restype = ctypes.c_int
         lib.pkv_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
         lib.pkv_device_error.restype = ctypes.c_int
+        for name, args in {
+            "pkv_kv_cache_write_q4": [vp, i64, vp, i64, vp, i32, vp, vp],
+            "pkv_kv_cache_read_q4": [vp, vp, i32, vp, vp, vp],
+            "pkv_paged_attn_decode_q4": [vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, sz, vp],
+            "pkv_paged_attn_prefill_q4": [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp, sz, vp],
+            "pkv_qk_norm_rope": [vp, i64, vp, i64, i32, i32, i32, i32, vp, vp, i64, vp, i64, vp],
+            "pkv_qk_norm_rope_write": [vp, i64, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp, i64,
+                                       vp],
+            "pkv_qk_norm_rope_write_q4": [vp, i64, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, i64, vp],
+            "pkv_fork_blocks": [vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp],
+            "pkv_free_blocks": [vp, vp, i32, i32, vp, i32, vp],
+            "pkv_compact_blocks": [vp, vp, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp],
+            "pkv_copy_blocks": [vp, i32, i64, i32, i64, vp, vp, i32, vp],
+        }.items():
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = ctypes.c_int
+        lib.pkv_decode_q4_workspace_bytes.argtypes = [i32, i32, i32]
+        lib.pkv_decode_q4_workspace_bytes.restype = sz
+        lib.pkv_prefill_q4_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+        lib.pkv_prefill_q4_workspace_bytes.restype = sz
         if path is None:
             _lib = lib
         return lib
@@ -389,9 +410,53 @@ def sample_exponential_race(logits: torch.Tensor, temperatures: torch.Tensor, se
     return out
 
 
+def _launch(fn: str, dev: torch.device, *args) -> None:
+    """Call `fn` of the library with `dev` current and its current stream as the last argument."""
+    lib = load()
+    if dev.index == torch.cuda.current_device():
+        _check(fn, getattr(lib, fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, getattr(lib, fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _same_device(dev: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _ints(dev: torch.device, **tensors) -> None:
+    """Contiguous int32 tensors on `dev`."""
+    for name, t in tensors.items():
+        _dev(t, name, torch.int32)
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t: torch.Tensor, name: str, heads: int | None = None, head_dim: int = 128):
+    """[N, heads, head_dim] bf16 with contiguous rows; returns (N, heads, token stride)."""
+    _dev(t, name, torch.bfloat16)
+    if t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [N, {'heads' if heads is None else heads}, {head_dim}]")
+    n, h = int(t.shape[0]), int(t.shape[1])
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name} must have contiguous rows")
+    return n, h, t.stride(0) if n > 1 else h * head_dim
+
+
 def device_error(clear: bool = True) -> list[str]:
     """Names of the device error bits set since the last clear (synchronises)."""
     lib = load()
     v = ctypes.c_uint32(0)
     _check("pkv_device_error", lib.pkv_device_error(ctypes.byref(v), 1 if clear else 0))
     return [name for bit, name in DEVERR.items() if v.value & bit]
+
+
+from .blocks import compact_blocks, copy_blocks, fork_blocks, free_blocks  # noqa: E402
+from .q4 import (Q4Cache, decode_q4_workspace, kv_cache_read_q4, kv_cache_write_q4,  # noqa: E402
+                 paged_attn_decode_q4, paged_attn_prefill_q4, prefill_q4_workspace)
+from .rope import (qk_norm_rope, qk_norm_rope_write, qk_norm_rope_write_q4,  # noqa: E402
+                   rope_frequencies)

@@ -1,0 +1,311 @@
+// blocks.cu -- forking, freeing and compacting the blocks of a paged cache, and
+// copying blocks.
+//
+// The bookkeeping is a block table and a length per sequence and a reference
+// count per block (0 = free).
+//   fork     a child shares its parent's full blocks (counts + 1) and gets a
+//            free block of its own for the last, partly filled one, to be copied;
+//            the i-th child that needs a block gets the i-th smallest free id.
+//   free     every block of a sequence loses one reference.
+//   compact  with n live blocks, the i-th smallest live id >= n moves into the
+//            i-th smallest free id < n; tables and counts follow.
+// All three are integer work whose result does not depend on the order in which
+// threads run.  Fork and the compaction plan need ranks over all blocks: one CTA
+// scans the counts (a pool has some ten thousand blocks), which costs less than
+// the extra launches of a scan over several CTAs.
+//   copy     whole blocks in every plane (layer, K or V) of a cache; bound by HBM.
+#include <cuda_runtime.h>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace {
+
+__device__ unsigned int g_err_blocks;
+
+constexpr int kScanThreads = 1024;
+
+__device__ __forceinline__ int blocks_of(int len) { return (len + kBlockSize - 1) / kBlockSize; }
+
+// Exclusive prefix sum of one value per thread over the CTA; *total gets the
+// sum.  Two barriers; `warp_sums` holds 32 words.
+__device__ __forceinline__ int cta_exclusive_scan(int x, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();  // the previous call's readers are done
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  int w = warp_sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return incl - x + (warp ? before : 0);
+}
+
+__global__ void __launch_bounds__(kScanThreads) fork_kernel(const ForkArgs p) {
+  __shared__ int free_ids[kMaxForks];
+  __shared__ int warp_sums[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long cap = static_cast<long long>(p.max_blocks_per_seq) * kBlockSize;
+  // Which children can be made: child_lens = the length, or 0.
+  for (int i = warp; i < p.num_forks; i += kScanThreads / 32) {
+    const int parent = p.parents[i];
+    int len = 0;
+    if (parent >= 0 && parent < p.num_seqs) len = p.context_lens[parent];
+    if (parent < 0 || parent >= p.num_seqs || len < 0 || len > cap) {
+      if (lane == 0) atomicOr(&g_err_blocks, PKV_DEVERR_LEN_RANGE);
+      len = 0;
+    }
+    bool bad = false;
+    for (int j = lane; j < blocks_of(len); j += 32) {
+      const int b = p.block_tables[static_cast<int64_t>(parent) * p.max_blocks_per_seq + j];
+      if (b < 0 || b >= p.num_blocks || p.ref_count[b] <= 0) bad = true;
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+      if (lane == 0) atomicOr(&g_err_blocks, PKV_DEVERR_BLOCK_RANGE);
+      len = 0;
+    }
+    if (lane == 0) p.child_lens[i] = len;
+  }
+  __syncthreads();
+  // Rank of every child that needs a block of its own (kept in copy_dst).
+  int needed = 0;
+  for (int base = 0; base < p.num_forks; base += kScanThreads) {
+    const int i = base + threadIdx.x;
+    const int need = i < p.num_forks && p.child_lens[i] % kBlockSize != 0;
+    int total;
+    const int rank = needed + cta_exclusive_scan(need, warp_sums, &total);
+    if (i < p.num_forks) p.copy_dst[i] = need ? rank : -1;
+    needed += total;
+  }
+  // The first `needed` free ids, ascending.
+  int found = 0;
+  for (int base = 0; base < p.num_blocks && found < needed; base += kScanThreads) {
+    const int id = base + threadIdx.x;
+    const int is_free = id < p.num_blocks && p.ref_count[id] == 0;
+    int total;
+    const int rank = found + cta_exclusive_scan(is_free, warp_sums, &total);
+    if (is_free && rank < needed) free_ids[rank] = id;
+    found += total;
+  }
+  __syncthreads();
+  for (int i = warp; i < p.num_forks; i += kScanThreads / 32) {
+    const int parent = p.parents[i];
+    int len = p.child_lens[i];
+    const int rank = p.copy_dst[i];
+    if (rank >= found) {
+      if (lane == 0) atomicOr(&g_err_blocks, PKV_DEVERR_NO_BLOCKS);
+      len = 0;
+    }
+    const int used = blocks_of(len);
+    const int64_t row = static_cast<int64_t>(i) * p.max_blocks_per_seq;
+    __syncwarp();
+    for (int j = lane; j < p.max_blocks_per_seq; j += 32) {
+      int b = -1;
+      if (j < used) {
+        b = p.block_tables[static_cast<int64_t>(parent) * p.max_blocks_per_seq + j];
+        if (j == used - 1 && len % kBlockSize != 0) {
+          p.copy_src[i] = b;
+          b = free_ids[rank];
+          p.copy_dst[i] = b;
+        }
+        atomicAdd(p.ref_count + b, 1);
+      }
+      p.child_tables[row + j] = b;
+    }
+    if (lane == 0) {
+      p.child_lens[i] = len;
+      if (len % kBlockSize == 0) p.copy_src[i] = p.copy_dst[i] = -1;
+    }
+  }
+}
+
+constexpr int kRowWarps = 4;
+
+__global__ void __launch_bounds__(32 * kRowWarps)
+    free_kernel(const int32_t* __restrict__ tables, const int32_t* __restrict__ lens, int num_seqs, int maxb,
+                int32_t* ref_count, int num_blocks) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  for (int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5); r < num_seqs; r += gridDim.x * kRowWarps) {
+    const int len = lens[r];
+    if (len < 0 || len > static_cast<long long>(maxb) * kBlockSize) {
+      if (lane == 0) atomicOr(&g_err_blocks, PKV_DEVERR_LEN_RANGE);
+      continue;
+    }
+    for (int j = lane; j < blocks_of(len); j += 32) {
+      const int b = tables[static_cast<int64_t>(r) * maxb + j];
+      if (b < 0 || b >= num_blocks) {
+        atomicOr(&g_err_blocks, PKV_DEVERR_BLOCK_RANGE);
+      } else if (atomicSub(ref_count + b, 1) <= 0) {
+        // Not held: the count stays at zero.  (A count only goes below zero once
+        // it is used up, so a reference that exists is always given back.)
+        atomicAdd(ref_count + b, 1);
+        atomicOr(&g_err_blocks, PKV_DEVERR_REF_COUNT);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const CompactArgs p) {
+  __shared__ int warp_sums[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  int mine = 0;
+  for (int id = threadIdx.x; id < p.num_blocks; id += kScanThreads) mine += p.ref_count[id] > 0;
+  int live;
+  cta_exclusive_scan(mine, warp_sums, &live);
+  // Holes below `live` and movers from `live` on are equally many.
+  int holes = 0, movers = 0;
+  for (int base = 0; base < p.num_blocks; base += kScanThreads) {
+    const int id = base + threadIdx.x;
+    const int ref = id < p.num_blocks ? p.ref_count[id] : 0;
+    const bool hole = id < live && ref <= 0, mover = id >= live && ref > 0;
+    int total;
+    const int rank = cta_exclusive_scan((hole ? 1 : 0) | (mover ? 0x10000 : 0), warp_sums, &total);
+    if (hole) p.copy_dst[holes + (rank & 0xffff)] = id;
+    if (mover) p.copy_src[movers + (rank >> 16)] = id;
+    // Movers' counts are read again below, so they stay (the outputs may be the inputs).
+    if (id < p.num_blocks && !hole && !mover) p.new_ref_count[id] = ref > 0 ? ref : 0;
+    holes += total & 0xffff;
+    movers += total >> 16;
+  }
+  __syncthreads();
+  for (int m = threadIdx.x; m < p.num_blocks / 2; m += kScanThreads) {
+    if (m < movers) {
+      const int from = p.copy_src[m], to = p.copy_dst[m];
+      const int ref = p.ref_count[from];
+      p.new_ref_count[to] = ref;
+      p.new_ref_count[from] = 0;
+    } else {
+      p.copy_src[m] = p.copy_dst[m] = -1;
+    }
+  }
+  if (threadIdx.x == 0) *p.num_moves = movers;
+}
+
+// Entries of blocks that moved follow them: binary search in the ascending list
+// of movers.
+__global__ void __launch_bounds__(256) compact_tables_kernel(const CompactArgs p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t entries = static_cast<int64_t>(p.num_seqs) * p.max_blocks_per_seq;
+  const int moves = *p.num_moves;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < entries; e += gridDim.x * 256ll) {
+    const int r = static_cast<int>(e / p.max_blocks_per_seq);
+    const int j = static_cast<int>(e - static_cast<int64_t>(r) * p.max_blocks_per_seq);
+    const int len = p.context_lens[r];
+    int b = p.block_tables[e];
+    if (len < 0 || len > static_cast<long long>(p.max_blocks_per_seq) * kBlockSize) {
+      if (j == 0) atomicOr(&g_err_blocks, PKV_DEVERR_LEN_RANGE);
+    } else if (j < blocks_of(len)) {
+      if (b < 0 || b >= p.num_blocks) {
+        atomicOr(&g_err_blocks, PKV_DEVERR_BLOCK_RANGE);
+      } else if (moves > 0 && b >= p.copy_src[0]) {
+        int lo = 0, hi = moves - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (p.copy_src[mid] < b)
+            lo = mid + 1;
+          else
+            hi = mid;
+        }
+        if (p.copy_src[lo] == b)
+          b = p.copy_dst[lo];
+        else
+          atomicOr(&g_err_blocks, PKV_DEVERR_BLOCK_RANGE);  // a block that nothing holds
+      }
+    }
+    p.new_tables[e] = b;
+  }
+}
+
+// One CTA moves one 32 KiB piece at a time; each thread has eight 16-byte loads
+// in flight before its stores.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 8;
+constexpr int64_t kPieceVecs = static_cast<int64_t>(kCopyThreads) * kCopyUnroll;
+
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_kernel(uint4* cache, int num_planes, int64_t plane_vecs, int num_blocks, int64_t block_vecs,
+                const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int num_copies) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t pieces = (block_vecs + kPieceVecs - 1) / kPieceVecs;
+  const int64_t per_copy = pieces * num_planes;
+  const int64_t items = per_copy * num_copies;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int i = static_cast<int>(it / per_copy);
+    const int64_t rest = it - i * per_copy;
+    const int64_t plane = rest / pieces, piece = rest - plane * pieces;
+    const int from = __ldg(src + i), to = __ldg(dst + i);
+    if (from < 0 || to < 0 || from >= num_blocks || to >= num_blocks) {
+      if (!(from == -1 && to == -1) && threadIdx.x == 0) atomicOr(&g_err_blocks, PKV_DEVERR_BLOCK_RANGE);
+      continue;
+    }
+    if (from == to) continue;
+    const uint4* s = cache + plane * plane_vecs + from * block_vecs;
+    uint4* d = cache + plane * plane_vecs + to * block_vecs;
+    const int64_t v0 = piece * kPieceVecs + threadIdx.x;
+    uint4 r[kCopyUnroll];
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+      const int64_t v = v0 + u * kCopyThreads;
+      if (v < block_vecs) r[u] = s[v];
+    }
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+      const int64_t v = v0 + u * kCopyThreads;
+      if (v < block_vecs) d[v] = r[u];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_fork_blocks(const ForkArgs& a, cudaStream_t stream) {
+  return launch_pdl(fork_kernel, dim3(1), dim3(kScanThreads), 0, stream, a);
+}
+
+cudaError_t launch_free_blocks(const int32_t* block_tables, const int32_t* context_lens, int32_t num_seqs,
+                               int32_t max_blocks_per_seq, int32_t* ref_count, int32_t num_blocks, int num_sms,
+                               cudaStream_t stream) {
+  const int blocks = std::min((num_seqs + kRowWarps - 1) / kRowWarps, num_sms * 8);
+  return launch_pdl(free_kernel, dim3(blocks), dim3(32 * kRowWarps), 0, stream, block_tables, context_lens, num_seqs,
+                    max_blocks_per_seq, ref_count, num_blocks);
+}
+
+cudaError_t launch_compact_blocks(const CompactArgs& a, int num_sms, cudaStream_t stream) {
+  cudaError_t e = launch_pdl(compact_plan_kernel, dim3(1), dim3(kScanThreads), 0, stream, a);
+  if (e != cudaSuccess || a.num_seqs == 0) return e;
+  const int64_t entries = static_cast<int64_t>(a.num_seqs) * a.max_blocks_per_seq;
+  const int64_t blocks = std::min<int64_t>((entries + 255) / 256, static_cast<int64_t>(num_sms) * 8);
+  return launch_pdl(compact_tables_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, a);
+}
+
+cudaError_t launch_copy_blocks(void* cache, int32_t num_planes, int64_t plane_stride, int32_t num_blocks,
+                               int64_t block_bytes, const int32_t* src, const int32_t* dst, int32_t num_copies,
+                               int num_sms, cudaStream_t stream) {
+  const int64_t vecs = block_bytes / 16;
+  const int64_t items = (vecs + kPieceVecs - 1) / kPieceVecs * num_planes * num_copies;
+  const int64_t blocks = std::min<int64_t>(items, static_cast<int64_t>(num_sms) * 8);
+  return launch_pdl(copy_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kCopyThreads), 0, stream,
+                    static_cast<uint4*>(cache), num_planes, plane_stride / 16, num_blocks, vecs, src, dst, num_copies);
+}
+
+PKV_DEFINE_READ_ERROR(read_error_blocks, g_err_blocks)
+
+}  // namespace pkv

@@ -477,6 +477,12 @@ pkv_status pkv_device_error(uint32_t* out, int clear) {
   uint32_t e5 = 0;
   if (read_error_sampler(&e5, clear != 0) != cudaSuccess) return PKV_ERR_CUDA;
   *out = a | b | c | d | e5;
+  for (auto read : {read_error_kv_q4, read_error_decode_q4, read_error_prefill_q4, read_error_norm_rope,
+                    read_error_blocks}) {
+    uint32_t more = 0;
+    if (read(&more, clear != 0) != cudaSuccess) return PKV_ERR_CUDA;
+    *out |= more;
+  }
   return PKV_OK;
 }
 

@@ -170,7 +170,127 @@ struct SampleArgs {
 size_t sample_workspace_bytes(int batch, int vocab);
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream);
 
+// ---- the 4-bit cache (format in q4_device.cuh)
+struct Q4Cache {
+  uint8_t* k_data;    // [num_blocks, 256, Hkv, 64]
+  uint8_t* k_scales;  // [num_blocks, 256, Hkv, 8]
+  uint8_t* v_data;
+  uint8_t* v_scales;
+  float k_scale, v_scale;  // tensor scales
+  float k_inv, v_inv;      // their reciprocals, rounded to fp32
+  int32_t num_blocks, num_kv_heads;
+};
+cudaError_t launch_kv_write_q4(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                               const int32_t* slots, int32_t num_tokens, const Q4Cache& c, int num_sms,
+                               cudaStream_t stream);
+cudaError_t launch_kv_read_q4(const int32_t* slots, int32_t num_tokens, const Q4Cache& c, uint16_t* k, uint16_t* v,
+                              int num_sms, cudaStream_t stream);
+
+// ---- attention over the 4-bit cache
+struct AttnQ4Args {
+  const uint16_t* q;
+  uint16_t* out;
+  const int32_t* context_lens;  // decode
+  const int32_t* cu_seqlens_q;  // prefill
+  const int32_t* cu_seqlens_k;  // prefill
+  const int32_t* block_tables;
+  int32_t max_blocks_per_seq;
+  int32_t num_seqs, total_q, max_seqlen_q, max_seqlen_k;  // decode: batch rows, max_context_len
+  int32_t num_q_heads;
+  float scale;
+  void* workspace;
+  Q4Cache cache;
+};
+size_t decode_q4_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_sms);
+size_t prefill_q4_workspace_bytes(int total_q, int num_seqs, int max_seqlen_q, int max_seqlen_k, int num_q_heads,
+                                  int num_kv_heads, int num_sms);
+cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream);
+
+// ---- norm + rotation of queries and keys
+struct NormRopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_stride, k_stride, v_stride;
+  int32_t num_tokens, num_q_heads, num_kv_heads;
+  const uint16_t* q_weight;  // null: rows are not normalised
+  const uint16_t* k_weight;
+  float eps;
+  const int64_t* freqs;      // [rope_dim / 2] turns per position, Q0.64
+  int32_t rope_dim, interleaved;
+  const int32_t* positions;  // axis a of token t at a * position_axis_stride + t
+  int64_t position_axis_stride;
+  int32_t section_end0, section_end1;  // pairs below end0 follow axis 0, below end1 axis 1, else axis 2
+  uint16_t* q_out;
+  int64_t q_out_stride;
+  uint16_t* k_out;  // dest 0
+  int64_t k_out_stride;
+  const int32_t* slots;  // dest 1, 2
+  int32_t num_blocks;
+  uint16_t* k_cache;  // dest 1
+  uint16_t* v_cache;
+  Q4Cache q4;  // dest 2
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int dest, int num_sms, cudaStream_t stream);
+
+// ---- blocks of a cache
+struct ForkArgs {
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  int32_t num_seqs, max_blocks_per_seq;
+  const int32_t* parents;
+  int32_t num_forks;
+  int32_t* ref_count;
+  int32_t num_blocks;
+  int32_t* child_tables;
+  int32_t* child_lens;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+};
+constexpr int kMaxForks = 8192;
+cudaError_t launch_fork_blocks(const ForkArgs& a, cudaStream_t stream);
+cudaError_t launch_free_blocks(const int32_t* block_tables, const int32_t* context_lens, int32_t num_seqs,
+                               int32_t max_blocks_per_seq, int32_t* ref_count, int32_t num_blocks, int num_sms,
+                               cudaStream_t stream);
+struct CompactArgs {
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  int32_t num_seqs, max_blocks_per_seq;
+  const int32_t* ref_count;
+  int32_t num_blocks;
+  int32_t* new_tables;
+  int32_t* new_ref_count;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* num_moves;
+};
+cudaError_t launch_compact_blocks(const CompactArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_copy_blocks(void* cache, int32_t num_planes, int64_t plane_stride, int32_t num_blocks,
+                               int64_t block_bytes, const int32_t* src, const int32_t* dst, int32_t num_copies,
+                               int num_sms, cudaStream_t stream);
+
+// Defines cudaError_t name(uint32_t* out, bool clear): read, and on request
+// reset, the device error word `word` of a translation unit.
+#define PKV_DEFINE_READ_ERROR(name, word)                                     \
+  cudaError_t name(uint32_t* out, bool clear) {                               \
+    unsigned int v = 0;                                                       \
+    cudaError_t e = cudaMemcpyFromSymbol(&v, word, sizeof v);                 \
+    if (e != cudaSuccess) return e;                                           \
+    *out = v;                                                                 \
+    if (clear) {                                                              \
+      const unsigned int zero = 0;                                            \
+      e = cudaMemcpyToSymbol(word, &zero, sizeof zero);                       \
+    }                                                                         \
+    return e;                                                                 \
+  }
+
 // ---- device error words (one per translation unit)
+cudaError_t read_error_kv_q4(uint32_t* out, bool clear);
+cudaError_t read_error_decode_q4(uint32_t* out, bool clear);
+cudaError_t read_error_prefill_q4(uint32_t* out, bool clear);
+cudaError_t read_error_norm_rope(uint32_t* out, bool clear);
+cudaError_t read_error_blocks(uint32_t* out, bool clear);
 cudaError_t read_error_kv_write(uint32_t* out, bool clear);
 cudaError_t read_error_decode(uint32_t* out, bool clear);
 cudaError_t read_error_prefill(uint32_t* out, bool clear);

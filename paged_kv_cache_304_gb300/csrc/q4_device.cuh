@@ -1,0 +1,99 @@
+// q4_device.cuh -- the 4-bit row format on the device.
+//
+// A row of 128 dims of one head is eight groups of 16 consecutive dims.  Group
+// j holds a scale s_j (e4m3, one byte) and 16 codes (e2m1, two to a byte, the
+// even dim in the low nibble); dim d stands for code_d * s_j * tensor_scale.
+//   quantising   y = x * (1 / tensor_scale) in fp32,
+//                s = e4m3(min(max|y| / 6, 448)), round to nearest even,
+//                code = e2m1(y / s), round to nearest even, saturating at 6;
+//                s == 0 gives codes 0 (a group below 2^-10 * 6 reads as zero);
+//                a NaN in the group makes its scale NaN, so all 16 read as NaN;
+//                an infinity reads as +-6 * 448 * tensor_scale.
+// code * s has at most six significant bits: it is exact in fp16 and in bf16,
+// so attention over the cache multiplies the held values themselves, and
+// tensor_scale is applied in fp32 outside the products.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+namespace q4 {
+
+constexpr int kGroup = 16;       // dims that share a scale
+constexpr int kRowBytes = 64;    // codes of one head's row
+constexpr int kRowScales = 8;    // scales of one head's row
+
+// Two codes from two floats: `lo` in bits 0-3.
+__device__ __forceinline__ uint32_t enc2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The four bytes of a word as four fp16 pairs: out[i] = codes 2i (low half), 2i+1.
+__device__ __forceinline__ void dec8(uint32_t w, uint32_t (&out)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+      : "r"(w));
+}
+
+// e4m3 byte of a float (round to nearest even, saturating; NaN stays NaN).
+__device__ __forceinline__ uint32_t enc_scale(float s) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(s));
+  return r & 0xffu;
+}
+
+// Two e4m3 bytes (low 16 bits) as an fp16 pair.
+__device__ __forceinline__ uint32_t dec_scale2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+
+__device__ __forceinline__ float half_lo(uint32_t h2) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xffffu)));
+}
+__device__ __forceinline__ float half_hi(uint32_t h2) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 >> 16)));
+}
+__device__ __forceinline__ float dec_scale(uint32_t byte) { return half_lo(dec_scale2(byte)); }
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Maximum that a NaN wins.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Scale byte of a group whose largest |y| is `amax`.
+__device__ __forceinline__ uint32_t group_scale(float amax) { return enc_scale(__fdiv_rn(amax, 6.f)); }
+
+// Eight codes of eight floats y over scale s (as the float its byte stands for).
+__device__ __forceinline__ uint32_t enc8(const float* y, float s) {
+  uint32_t w = 0;
+  if (s == 0.f) return 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w |= enc2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)) << (8 * i);
+  return w;
+}
+
+// bf16 pair word to two floats (exact).
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+}  // namespace q4
+}  // namespace pkv

@@ -1,0 +1,195 @@
+"""Forking, freeing, compacting and copying blocks against plain Python."""
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_304_gb300 as pkv
+from tests.gpu_util import dev, i32
+
+pytestmark = pytest.mark.gpu
+BS = 256
+
+
+def pool(lens, nb, maxb, seed=0, spare=7):
+    """Tables (rows filled behind with `spare`, which nothing may read) and counts."""
+    rng = np.random.default_rng(seed)
+    perm = list(rng.permutation(nb))
+    tab = np.full((len(lens), maxb), spare, np.int32)
+    ref = np.zeros(nb, np.int32)
+    for r, n in enumerate(lens):
+        for j in range(-(-n // BS)):
+            tab[r, j] = perm.pop()
+            ref[tab[r, j]] += 1
+    return tab, np.asarray(lens, np.int32), ref
+
+
+def fork_ref(tab, lens, parents, ref):
+    ref = ref.copy()
+    S, maxb = tab.shape
+    nb = ref.size
+    free = [b for b in range(nb) if ref[b] == 0]
+    child, clen = np.full((len(parents), maxb), -1, np.int32), np.zeros(len(parents), np.int32)
+    src, dst = np.full(len(parents), -1, np.int32), np.full(len(parents), -1, np.int32)
+    errs, held = set(), ref.copy()
+    for i, p in enumerate(parents):
+        if not 0 <= p < S or not 0 <= lens[p] <= maxb * BS:
+            errs.add("LEN_RANGE")
+            continue
+        used = -(-int(lens[p]) // BS)
+        row = tab[p, :used]
+        if any(b < 0 or b >= nb or held[b] <= 0 for b in row):
+            errs.add("BLOCK_RANGE")
+            continue
+        new = row.copy()
+        if lens[p] % BS:
+            if not free:
+                errs.add("NO_BLOCKS")
+                continue
+            src[i], dst[i] = row[-1], free.pop(0)
+            new[-1] = dst[i]
+        child[i, :used], clen[i] = new, lens[p]
+        for b in new:
+            ref[b] += 1
+    return child, clen, src, dst, ref, errs
+
+
+def run_fork(tab, lens, parents, ref):
+    d_ref = i32(ref)
+    pkv.device_error(clear=True)
+    got = pkv.fork_blocks(i32(tab), i32(lens), i32(parents), d_ref)
+    exp = fork_ref(tab, lens, parents, ref)
+    assert set(pkv.device_error()) == exp[5]
+    for g, e, n in zip((*got, d_ref), exp, ("tables", "lens", "src", "dst", "ref")):
+        assert np.array_equal(g.cpu().numpy(), e), n
+    return got, d_ref
+
+
+@pytest.mark.parametrize("lens,parents", [
+    ([300], [0]), ([256], [0, 0]), ([0, 1], [0, 1, 1]), ([257, 512, 1, 900], [3, 0, 3, 1, 2, 2, 3]),
+    ([100 + 37 * i for i in range(20)], list(range(20)) * 3)])
+def test_fork(lens, parents):
+    tab, ln, ref = pool(lens, 200, 5)
+    (tables, clens, src, dst), d_ref = run_fork(tab, ln, parents, ref)
+    # freeing the children gives the counts back
+    pkv.free_blocks(tables, clens, d_ref)
+    assert np.array_equal(d_ref.cpu().numpy(), ref) and pkv.device_error() == []
+
+
+def test_fork_many_children_and_a_large_pool():
+    tab, ln, ref = pool([1000, 10, 2049, 256], 20000, 9, 3)
+    run_fork(tab, ln, list(np.random.default_rng(1).integers(0, 4, 5000)), ref)
+
+
+def test_fork_runs_out_of_blocks():
+    tab, ln, ref = pool([300, 512, 10], 7, 3)  # five held, two free
+    run_fork(tab, ln, [0, 1, 2, 0, 1], ref)
+
+
+def test_fork_of_bad_parents():
+    tab, ln, ref = pool([300, 512, 10, 700], 16, 3)
+    tab[1, 1] = 99
+    ln[3] = 3 * BS + 1
+    free = int(np.nonzero(ref == 0)[0][0])
+    tab[2, 0] = free  # a block that nothing holds
+    run_fork(tab, ln, [0, 1, 2, 3, -1, 4, 0], ref)
+
+
+def test_free_flags_what_is_not_held():
+    tab, ln, ref = pool([300, 10, 40], 8, 2)
+    d = i32(ref)
+    rows, lens = i32(np.concatenate([tab, tab[:1], [[99, 0], [0, 0]]])), i32([*ln, ln[0], 5, 999])
+    pkv.device_error(clear=True)
+    pkv.free_blocks(rows, lens, d)
+    assert set(pkv.device_error()) == {"REF_COUNT", "BLOCK_RANGE", "LEN_RANGE"}
+    assert (d == 0).all()
+
+
+def compact_ref(tab, lens, ref):
+    nb = ref.size
+    live = [b for b in range(nb) if ref[b] > 0]
+    n = len(live)
+    src = [b for b in live if b >= n]
+    dst = [b for b in range(n) if ref[b] <= 0]
+    new_ref = np.where(ref > 0, ref, 0)
+    to = {}
+    for s, d in zip(src, dst):
+        new_ref[d], new_ref[s], to[s] = ref[s], 0, d
+    out = tab.copy()
+    for r in range(tab.shape[0]):
+        for j in range(-(-int(lens[r]) // BS)):
+            out[r, j] = to.get(int(tab[r, j]), tab[r, j])
+    pad = [-1] * (nb // 2 - len(src))
+    return out, new_ref, np.array(src + pad, np.int32), np.array(dst + pad, np.int32), np.array([len(src)], np.int32)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,nb,maxb", [([1], 1, 1), ([], 5, 2), ([0, 0], 6, 2), ([300, 5, 900], 40, 4),
+                                          ([256 * 4] * 30, 121, 4), ([10 * i for i in range(300)], 5000, 12)])
+def test_compact(lens, nb, maxb, in_place):
+    tab, ln, ref = pool(lens, nb, maxb, 5) if lens else (np.zeros((0, maxb), np.int32), np.zeros(0, np.int32),
+                                                         np.zeros(nb, np.int32))
+    dt, dr, dl = i32(tab), i32(ref), i32(ln)
+    out = (dt, dr, i32(np.zeros(nb // 2)), i32(np.zeros(nb // 2)), i32([0])) if in_place else None
+    pkv.device_error(clear=True)
+    got = pkv.compact_blocks(dt, dl, dr, out=out)
+    for g, e, n in zip(got, compact_ref(tab, ln, ref), ("tables", "ref", "src", "dst", "moves")):
+        assert np.array_equal(g.cpu().numpy(), e), n
+    if not in_place:
+        assert np.array_equal(dt.cpu().numpy(), tab) and np.array_equal(dr.cpu().numpy(), ref)
+    assert pkv.device_error() == []
+
+
+def test_compact_flags_bad_rows():
+    tab, ln, ref = pool([300, 10, 40], 16, 2, 1)
+    ref_bad = ref.copy()
+    tab2 = tab.copy()
+    tab2[0, 0] = 77
+    ln2 = ln.copy()
+    ln2[1] = -3
+    pkv.device_error(clear=True)
+    got = pkv.compact_blocks(i32(tab2), i32(ln2), i32(ref_bad))
+    assert set(pkv.device_error()) == {"BLOCK_RANGE", "LEN_RANGE"}
+    assert got[0][0, 0] == 77 and np.array_equal(got[0][1].cpu().numpy(), tab2[1])
+
+
+@pytest.mark.parametrize("shape,block_dim,dtype", [
+    ((9, 256, 2, 128), 0, torch.bfloat16), ((2, 3, 9, 256, 1, 64), 2, torch.uint8), ((4, 9, 16), 1, torch.uint8),
+    ((9, 5, 16), 0, torch.int32), ((2, 9, 65, 40), 1, torch.float32)])
+def test_copy(shape, block_dim, dtype):
+    g = torch.Generator().manual_seed(0)
+    x = torch.randint(0, 100, shape, generator=g).to(dtype)
+    d = x.to(dev())
+    src, dst = [1, -1, 3, 1, 8, 5], [0, -1, 2, 4, 7, 5]
+    pkv.device_error(clear=True)
+    pkv.copy_blocks(d, i32(src), i32(dst), block_dim)
+    exp = x.clone()
+    for s, t in zip(src, dst):
+        if s >= 0:
+            exp.select(block_dim, t).copy_(x.select(block_dim, s))
+    assert torch.equal(d.cpu(), exp) and pkv.device_error() == []
+
+
+def test_copy_flags_bad_pairs_and_does_the_others():
+    x = torch.arange(4 * 64, dtype=torch.int32).view(4, 64)
+    d = x.to(dev())
+    pkv.device_error(clear=True)
+    pkv.copy_blocks(d, i32([0, 4, 1, -1]), i32([3, 0, -2, 1]))
+    assert pkv.device_error() == ["BLOCK_RANGE"]
+    assert torch.equal(d.cpu()[3], x[0]) and torch.equal(d.cpu()[:3], x[:3])
+    pkv.copy_blocks(d, i32([]), i32([]))
+
+
+def test_binding_refusals():
+    tab, ln, ref = pool([300, 10], 8, 2)
+    with pytest.raises(TypeError):
+        pkv.fork_blocks(i32(tab).long(), i32(ln), i32([0]), i32(ref))
+    with pytest.raises(ValueError):
+        pkv.fork_blocks(i32(tab), i32(ln)[:1], i32([0]), i32(ref))
+    with pytest.raises(ValueError):
+        pkv.compact_blocks(i32(tab), i32(ln), i32(ref), out=(i32([0]),) * 5)
+    x = torch.zeros(4, 3, dtype=torch.int32, device=dev())
+    with pytest.raises(pkv.PkvError):
+        pkv.copy_blocks(x, i32([0]), i32([1]))  # blocks of 12 bytes
+    with pytest.raises(ValueError):
+        pkv.copy_blocks(x.t(), i32([0]), i32([1]))

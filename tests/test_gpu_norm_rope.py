@@ -1,0 +1,196 @@
+"""Norm + rotation on the GPU against the formula in 64 bits, alone and with the
+KV-cache write.
+
+Allowance: the output's rounding to bf16 is half a step, 2^-8 |y|.  The fp32
+part: the mean square over 128 dims and rsqrt are within 2^-20 relative, three
+products 2^-22, and the angle (its fraction of a turn rounded to fp32) within
+2 pi 2^-25 < 2^-22 rad plus sincospi's two units in the last place, 2^-22; a
+rotated value moves by at most that times the length of its pair: 2^-18 in all
+leaves room."""
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_304_gb300 as pkv
+from tests import q4_ref
+from tests.gpu_util import dev, i32
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+def make(n, hq, hkv, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    qkv = (torch.randn((n, hq + 2 * hkv, 128), generator=g) * 3).to(torch.bfloat16)
+    w = [(1 + 0.3 * torch.randn(128, generator=g)).to(torch.bfloat16) for _ in range(2)]
+    return qkv, w
+
+
+def reference(x, w, inv_freq, positions, axis, interleaved):
+    """x [n, h, 128]; returns (y, length of each dim's pair)."""
+    x = x.double()
+    if w is not None:
+        x = x / (x.square().mean(-1, keepdim=True) + EPS).sqrt() * w.double()
+    half = len(inv_freq)
+    y, size = x.clone(), x.abs().clone()
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        t = torch.as_tensor(positions[axis[i]].astype(np.float64)) * inv_freq[i]
+        c, s = t.cos()[:, None], t.sin()[:, None]
+        y[..., a] = x[..., a] * c - x[..., b] * s
+        y[..., b] = x[..., b] * c + x[..., a] * s
+        size[..., a] = size[..., b] = (x[..., a].square() + x[..., b].square()).sqrt()
+    return y, size
+
+
+def close(got, ref, size):
+    err = (got.double().cpu() - ref).abs()
+    tol = 2.0**-8 * ref.abs() + 2.0**-18 * size + 1e-30
+    assert torch.isfinite(got.float()).all() and (err <= tol).all(), float((err - tol).max())
+
+
+def frequencies(rot, base=1e4):
+    return [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot", [0, 32, 64, 96, 128])
+@pytest.mark.parametrize("n,hq,hkv", [(1, 16, 8), (7, 15, 3), (40, 1, 1), (3, 64, 8)])
+def test_matches_formula(n, hq, hkv, rot, interleaved):
+    qkv, (wq, wk) = make(n, hq, hkv, n + rot)
+    pos = np.random.default_rng(rot).integers(0, 5000, n).astype(np.int32)
+    d = qkv.to(dev())
+    freqs = pkv.rope_frequencies(rot, 1e4, dev()) if rot else None
+    q, k = pkv.qk_norm_rope(d[:, :hq], d[:, hq:hq + hkv], wq.to(dev()), wk.to(dev()), EPS, freqs, i32(pos), interleaved)
+    f, axis = frequencies(rot) if rot else [], [0] * 64
+    close(q, *reference(qkv[:, :hq], wq, f, pos[None], axis, interleaved))
+    close(k, *reference(qkv[:, hq:hq + hkv], wk, f, pos[None], axis, interleaved))
+    assert pkv.device_error() == []
+
+
+@pytest.mark.parametrize("positions", [[0, 1, 2**31 - 1, 10**6, 123456789, -1, -2**31]])
+def test_far_and_negative_positions(positions):
+    """The angle is exact at any position: the 64-bit reference reduces it in integers."""
+    n = len(positions)
+    qkv, (wq, wk) = make(n, 2, 1, 5)
+    d = qkv.to(dev())
+    freqs = pkv.rope_frequencies(128, 1e6, dev())
+    q, _ = pkv.qk_norm_rope(d[:, :2], d[:, 2:3], wq.to(dev()), wk.to(dev()), EPS, freqs, i32(positions))
+    x = qkv[:, :2].double()
+    x = x / (x.square().mean(-1, keepdim=True) + EPS).sqrt() * wq.double()
+    for i, f in enumerate(freqs.cpu().tolist()):
+        turn = torch.tensor([((p * f) % 2**64) / 2**64 for p in positions], dtype=torch.float64) * 2 * np.pi
+        c, s = turn.cos()[:, None], turn.sin()[:, None]
+        a, b = x[..., i].clone(), x[..., i + 64].clone()
+        x[..., i], x[..., i + 64] = a * c - b * s, b * c + a * s
+    size = torch.cat([(x[..., :64].square() + x[..., 64:].square()).sqrt()] * 2, -1)
+    close(q, x, size)
+
+
+@pytest.mark.parametrize("sections", [(16, 24, 24), (64, 0, 0), (0, 0, 64), (10, 54)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_position_axes(sections, interleaved):
+    n, axes = 33, len(sections)
+    qkv, (wq, wk) = make(n, 4, 2, 7)
+    pos = np.random.default_rng(3).integers(0, 900, (axes, n)).astype(np.int32)
+    d = qkv.to(dev())
+    q, k = pkv.qk_norm_rope(d[:, :4], d[:, 4:6], wq.to(dev()), wk.to(dev()), EPS, pkv.rope_frequencies(128, 1e4, dev()),
+                            i32(pos), interleaved, sections)
+    axis = sum(([a] * m for a, m in enumerate(sections)), [])
+    close(q, *reference(qkv[:, :4], wq, frequencies(128), pos, axis, interleaved))
+    close(k, *reference(qkv[:, 4:6], wk, frequencies(128), pos, axis, interleaved))
+
+
+def test_broadcast_axes_equal_one_axis():
+    n = 9
+    qkv, (wq, wk) = make(n, 4, 2, 8)
+    d, p = qkv.to(dev()), i32(np.arange(n) * 31)
+    f = pkv.rope_frequencies(128, 1e4, dev())
+    a = pkv.qk_norm_rope(d[:, :4], d[:, 4:6], wq.to(dev()), wk.to(dev()), EPS, f, p)
+    b = pkv.qk_norm_rope(d[:, :4], d[:, 4:6], wq.to(dev()), wk.to(dev()), EPS, f, p.expand(3, n), sections=(16, 24, 24))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_without_weights_only_rotates_and_zero_rows_stay_zero():
+    n = 5
+    qkv, (wq, _) = make(n, 4, 2, 9)
+    qkv[2] = 0
+    pos = np.arange(n, dtype=np.int32)
+    d = qkv.to(dev())
+    q, k = pkv.qk_norm_rope(d[:, :4], d[:, 4:6], wq.to(dev()), None, EPS, pkv.rope_frequencies(128, 1e4, dev()), i32(pos))
+    close(k, *reference(qkv[:, 4:6], None, frequencies(128), pos[None], [0] * 64, False))
+    assert (q[2] == 0).all() and (k[2] == 0).all()
+
+
+def test_in_place():
+    n, hq, hkv = 130, 16, 8
+    qkv, (wq, wk) = make(n, hq, hkv, 10)
+    d, f, p = qkv.to(dev()), pkv.rope_frequencies(128, 1e4, dev()), i32(np.arange(n))
+    q, k = pkv.qk_norm_rope(d[:, :hq], d[:, hq:hq + hkv], wq.to(dev()), wk.to(dev()), EPS, f, p)
+    e = d.clone()
+    pkv.qk_norm_rope(e[:, :hq], e[:, hq:hq + hkv], wq.to(dev()), wk.to(dev()), EPS, f, p, q_out=e[:, :hq],
+                     k_out=e[:, hq:hq + hkv])
+    assert torch.equal(e[:, :hq], q) and torch.equal(e[:, hq:hq + hkv], k)
+    assert torch.equal(e[:, hq + hkv:], d[:, hq + hkv:])
+
+
+@pytest.mark.parametrize("rot,interleaved", [(128, False), (64, False), (96, False), (32, True), (0, False)])
+@pytest.mark.parametrize("n,hq,hkv", [(1, 16, 8), (300, 15, 3), (2500, 4, 1)])
+def test_writes_equal_the_two_calls(n, hq, hkv, rot, interleaved):
+    """The fused writes leave exactly what qk_norm_rope and then the write leave."""
+    nb = n // 256 + 2
+    qkv, (wq, wk) = make(n, hq, hkv, n)
+    slots = np.random.default_rng(n).permutation(nb * 256)[:n].astype(np.int32)
+    slots[3::5] = -1
+    d, p = qkv.to(dev()), i32(np.arange(n) * 3)
+    f = pkv.rope_frequencies(rot, 1e4, dev()) if rot else None
+    q, k, v = d[:, :hq], d[:, hq:hq + hkv], d[:, hq + hkv:]
+    a = (wq.to(dev()), wk.to(dev()), EPS, f, p)
+    q1, k1 = pkv.qk_norm_rope(q, k, *a, interleaved=interleaved)
+    caches = [torch.full((2, nb, 256, hkv, 128), 7.0, dtype=torch.bfloat16, device=dev()) for _ in range(2)]
+    pkv.kv_cache_write(k1, v, i32(slots), caches[0][0], caches[0][1])
+    q2 = pkv.qk_norm_rope_write(q, k, v, *a, i32(slots), caches[1][0], caches[1][1], interleaved=interleaved)
+    assert torch.equal(q1, q2) and torch.equal(caches[0], caches[1])
+    q4 = [pkv.Q4Cache.empty(nb, hkv, dev(), 0.5, 1.7) for _ in range(2)]
+    pkv.kv_cache_write_q4(k1, v, i32(slots), q4[0])
+    q3 = pkv.qk_norm_rope_write_q4(q, k, v, *a, i32(slots), q4[1], interleaved=interleaved)
+    assert torch.equal(q1, q3)
+    for name in ("k_data", "k_scales", "v_data", "v_scales"):
+        assert torch.equal(getattr(q4[0], name), getattr(q4[1], name)), name
+    held = q4_ref.values(q4[1].v_data.cpu().view(-1, hkv, 64), q4[1].v_scales.cpu().view(-1, hkv, 8), 1.7)
+    ref = q4_ref.values(*q4_ref.quantise(qkv[:, hq + hkv:], 1.7), 1.7)
+    keep = slots >= 0
+    assert np.array_equal(held[slots[keep]], ref[keep])
+
+
+def test_bad_slot_flags_and_skips():
+    qkv, (wq, wk) = make(3, 4, 2, 1)
+    d = qkv.to(dev())
+    c = torch.zeros((2, 1, 256, 2, 128), dtype=torch.bfloat16, device=dev())
+    pkv.device_error(clear=True)
+    q = pkv.qk_norm_rope_write(d[:, :4], d[:, 4:6], d[:, 6:], wq.to(dev()), wk.to(dev()), EPS,
+                               pkv.rope_frequencies(128, 1e4, dev()), i32([0, 1, 2]), i32([256, 5, -7]), c[0], c[1])
+    assert pkv.device_error() == ["SLOT_RANGE"]
+    assert int((c[0] != 0).any(-1).any(-1).sum()) == 1 and (q != 0).all(-1).any()
+
+
+def test_binding_refusals():
+    qkv, (wq, wk) = make(3, 4, 2, 1)
+    d = qkv.to(dev())
+    f, p = pkv.rope_frequencies(128, 1e4, dev()), i32([0, 1, 2])
+    w = (wq.to(dev()), wk.to(dev()), EPS)
+    with pytest.raises(ValueError):
+        pkv.qk_norm_rope(d[:, :4], d[:2, 4:6], *w, f, p)
+    with pytest.raises(ValueError):
+        pkv.qk_norm_rope(d[:, :4], d[:, 4:6], *w, f, p[:2])
+    with pytest.raises(ValueError):
+        pkv.qk_norm_rope(d[:, :4], d[:, 4:6], *w, f, p.expand(3, 3))
+    with pytest.raises(pkv.PkvError):
+        pkv.qk_norm_rope(d[:, :4], d[:, 4:6], *w, f, p.expand(3, 3), sections=(16, 16, 16))
+    with pytest.raises(pkv.PkvError):
+        pkv.qk_norm_rope(d[:, :4], d[:, 4:6], *w, pkv.rope_frequencies(48, 1e4, dev()), p)
+    with pytest.raises(TypeError):
+        pkv.qk_norm_rope(d[:, :4].float(), d[:, 4:6], *w, f, p)
+    with pytest.raises(TypeError):
+        pkv.qk_norm_rope(d[:, :4], d[:, 4:6], *w, f.float(), p)

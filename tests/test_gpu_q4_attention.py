@@ -1,0 +1,234 @@
+"""Decode and prefill over the 4-bit cache on the GPU against 64-bit attention
+over the held values (tests/q4_ref.py derives the allowance)."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_304_gb300 as pkv
+from tests import q4_ref
+from tests.gpu_util import dev, i32
+
+pytestmark = pytest.mark.gpu
+SCALE = 1 / math.sqrt(128)
+
+
+class Pool:
+    """A 4-bit pool whose unused slots hold hostile bytes: NaN scales and the largest codes."""
+
+    def __init__(self, lens, hkv, seed=0, ts=(1.0, 1.0), extra=2, spread=1.0):
+        rng = np.random.default_rng(seed)
+        need = [-(-int(n) // 256) for n in lens]
+        self.nb, self.hkv, self.lens, self.ts = sum(need) + extra, hkv, lens, ts
+        perm = list(rng.permutation(self.nb))
+        self.tables = np.full((len(lens), max([1] + need) + 1), -1, np.int32)
+        d = np.full((2, self.nb, 256, hkv, 64), 0x7F, np.uint8)
+        s = np.full((2, self.nb, 256, hkv, 8), 0x7F, np.uint8)
+        self.held = []
+        for r, n in enumerate(lens):
+            for j in range(need[r]):
+                self.tables[r, j] = perm.pop()
+            at = self.tables[r, np.arange(n) // 256].astype(np.int64) * 256 + np.arange(n) % 256
+            pair = []
+            for kv in range(2):
+                x = torch.from_numpy(rng.standard_normal((n, hkv, 128)).astype(np.float32) * spread)
+                x[..., 3::41] *= 5
+                data, scales = q4_ref.quantise(x.to(torch.bfloat16), ts[kv])
+                d[kv].reshape(-1, hkv, 64)[at] = data
+                s[kv].reshape(-1, hkv, 8)[at] = scales
+                pair.append(q4_ref.values(data, scales, ts[kv]))
+            self.held.append(pair)
+        self.d, self.s = torch.from_numpy(d).to(dev()), torch.from_numpy(s).to(dev())
+        self.cache = pkv.Q4Cache(self.d[0], self.s[0], self.d[1], self.s[1], *ts)
+
+
+def queries(n, hq, seed, size=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn((n, hq, 128), generator=g) * size).to(torch.bfloat16)
+
+
+def decode_case(lens, hq, hkv, seed=0, ts=(1.0, 1.0), pad=0, scale=SCALE, size=1.0, spread=1.0, **kw):
+    p = Pool(lens, hkv, seed, ts, spread=spread)
+    tables = np.concatenate([p.tables, np.full((pad, p.tables.shape[1]), -1, np.int32)])
+    q = queries(len(lens) + pad, hq, seed + 1, size)
+    pkv.device_error(clear=True)
+    out = pkv.paged_attn_decode_q4(q.to(dev()), p.cache, i32(list(lens) + [0] * pad), i32(tables), scale, **kw)
+    assert pkv.device_error() == []
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert (out[b] == 0).all()
+            continue
+        ref, tol = q4_ref.attention(q[b:b + 1].double(), p.held[b][0], p.held[b][1], scale, n)
+        q4_ref.check(out[b:b + 1], ref, tol, f"sequence {b} of length {n}")
+    assert (out[len(lens):] == 0).all()
+    return p, q, out
+
+
+EDGES = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 129, 255, 256, 257, 511, 513, 770, 0, 3]
+
+
+@pytest.mark.parametrize("hq,hkv", [(16, 8), (32, 8), (64, 8), (16, 1), (8, 1), (15, 3), (9, 1), (14, 7), (8, 8), (20, 2)])
+def test_decode_edge_lengths_and_groups(hq, hkv):
+    decode_case(EDGES, hq, hkv, seed=hq + hkv, pad=2)
+
+
+@pytest.mark.parametrize("lens", [[1], [4000], [20000], [1] * 300, [700] * 152, [5000, 1, 1, 9000, 2]])
+def test_decode_batch_shapes(lens):
+    decode_case(lens, 4, 2, seed=len(lens))
+
+
+@pytest.mark.parametrize("ts", [(0.25, 4.0), (0.37, 1.9)])
+def test_decode_tensor_scales(ts):
+    decode_case([300, 40, 600], 8, 4, ts=ts)
+
+
+def test_decode_large_and_tiny_queries():
+    """Query magnitudes far from one (beyond fp16) keep their precision."""
+    for size in (1e-6, 3e4, 1e9):
+        decode_case([300, 17], 8, 4, size=size, scale=SCALE / size)
+
+
+def test_decode_sharp_softmax():
+    decode_case([900, 300], 8, 4, scale=3.0)
+
+
+def test_decode_equal_keys_give_the_mean():
+    """Zero queries: every key weighs the same, across tiles, blocks and CTAs."""
+    p = Pool([5000], 2, 3)
+    q = torch.zeros((1, 4, 128), dtype=torch.bfloat16)
+    out = pkv.paged_attn_decode_q4(q.to(dev()), p.cache, i32([5000]), i32(p.tables), SCALE)
+    ref, tol = q4_ref.attention(q.double(), p.held[0][0], p.held[0][1], SCALE, 5000)
+    q4_ref.check(out, ref, tol, "mean")
+
+
+def test_decode_is_repeatable_and_takes_its_own_workspace():
+    p, q, out = decode_case([3000, 10, 777], 16, 8, seed=4)
+    ws = pkv.decode_q4_workspace(3, 16, 8, dev())
+    ws.fill_(0xAB)
+    for _ in range(3):
+        again = pkv.paged_attn_decode_q4(q.to(dev()), p.cache, i32(p.lens), i32(p.tables), SCALE, workspace=ws)
+        assert torch.equal(again, out)
+
+
+def test_decode_shared_blocks():
+    """Two sequences that share their first blocks read the same rows."""
+    p = Pool([600, 600], 2, 6)
+    p.tables[1, 0] = p.tables[0, 0]
+    q = queries(2, 4, 3)
+    out = pkv.paged_attn_decode_q4(q.to(dev()), p.cache, i32([600, 600]), i32(p.tables), SCALE)
+    k = [np.concatenate([p.held[0][kv][:256], p.held[1][kv][256:]]) for kv in range(2)]
+    ref, tol = q4_ref.attention(q[1:].double(), k[0], k[1], SCALE, 600)
+    q4_ref.check(out[1:], ref, tol, "shared")
+
+
+def test_decode_flags_bad_blocks_and_lengths():
+    p = Pool([300, 40], 2, 7)
+    q = queries(2, 4, 3).to(dev())
+    bad = p.tables.copy()
+    bad[0, 1] = 10**6
+    pkv.device_error(clear=True)
+    out = pkv.paged_attn_decode_q4(q, p.cache, i32([300, 40]), i32(bad), SCALE)
+    assert pkv.device_error() == ["BLOCK_RANGE"]
+    good = pkv.paged_attn_decode_q4(q, p.cache, i32([300, 40]), i32(p.tables), SCALE)
+    assert torch.equal(out[1], good[1])
+    out = pkv.paged_attn_decode_q4(q, p.cache, i32([300, -4]), i32(p.tables), SCALE, max_context_len=200)
+    assert pkv.device_error() == ["LEN_RANGE"]
+    assert (out[1] == 0).all()
+    ref, tol = q4_ref.attention(q[:1].double().cpu(), p.held[0][0][:200], p.held[0][1][:200], SCALE, 200)
+    q4_ref.check(out[:1], ref, tol, "clamped")
+
+
+def prefill_case(prompts, hq, hkv, seed=0, ts=(1.0, 1.0), scale=SCALE, size=1.0, bound=0, tail=0):
+    """prompts: (length, cached).  `bound` is added to the stated maxima, `tail` rows follow the last sequence."""
+    lens = [n for n, _ in prompts]
+    new = [n - c for n, c in prompts]
+    p = Pool(lens, hkv, seed, ts)
+    cu_q = np.concatenate([[0], np.cumsum(new)])
+    q = queries(int(cu_q[-1]) + tail, hq, seed + 1, size)
+    out = torch.full(q.shape, 77.0, dtype=torch.bfloat16, device=dev())
+    pkv.device_error(clear=True)
+    pkv.paged_attn_prefill_q4(q.to(dev()), p.cache, i32(cu_q), i32(np.concatenate([[0], np.cumsum(lens)])),
+                              i32(p.tables), scale, max(new) + bound, max(lens) + bound, out=out)
+    assert pkv.device_error() == []
+    for i, (n, c) in enumerate(prompts):
+        if n == c:
+            continue
+        rows = slice(int(cu_q[i]), int(cu_q[i + 1]))
+        ref, tol = q4_ref.attention(q[rows].double(), p.held[i][0], p.held[i][1], scale, c + 1)
+        q4_ref.check(out[rows], ref, tol, f"sequence {i} of {n} tokens, {c} cached")
+    assert (out[int(cu_q[-1]):] == 77).all()
+    return p, q, out
+
+
+@pytest.mark.parametrize("hq,hkv", [(16, 8), (4, 4), (3, 1), (16, 1), (15, 3), (32, 8)])
+def test_prefill_ragged(hq, hkv):
+    prompts = [(1, 0), (2, 1), (127, 0), (128, 0), (129, 0), (300, 256), (257, 256), (511, 100), (640, 0), (5, 5)]
+    prefill_case(prompts, hq, hkv, seed=hq, tail=3)
+
+
+@pytest.mark.parametrize("prompts", [[(1, 0)], [(1000, 999)], [(1500, 0)], [(3001, 2990), (4000, 3984)],
+                                     [(20000, 19995)], [(9000, 8800), (3, 0)], [(700, 0)] * 12])
+def test_prefill_shapes(prompts):
+    prefill_case(prompts, 4, 2, seed=len(prompts), bound=7)
+
+
+@pytest.mark.parametrize("ts", [(0.25, 4.0), (0.37, 1.9)])
+def test_prefill_tensor_scales(ts):
+    prefill_case([(300, 0), (40, 30)], 4, 2, ts=ts)
+
+
+def test_prefill_large_and_tiny_queries():
+    for size in (1e-6, 3e4, 1e9):
+        prefill_case([(200, 0), (300, 290)], 4, 2, size=size, scale=SCALE / size)
+
+
+def test_prefill_sharp_softmax():
+    prefill_case([(900, 0), (2000, 1990)], 4, 2, scale=3.0)
+
+
+def test_prefill_flags_and_skips_what_is_out_of_bounds():
+    p = Pool([300, 500, 40], 2, 7)
+    q = queries(140, 4, 3).to(dev())
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device=dev())
+    cu_q, cu_k = i32([0, 100, 110, 140]), i32([0, 300, 290, 330])  # the second has fewer keys than rows
+    pkv.device_error(clear=True)
+    pkv.paged_attn_prefill_q4(q, p.cache, cu_q, cu_k, i32(p.tables), SCALE, 100, 500, out=out)
+    assert pkv.device_error() == ["LEN_RANGE"]
+    assert (out[100:110] == 5).all() and (out[:100] != 5).any(-1).all() and (out[110:] != 5).any(-1).all()
+    out.fill_(5.0)
+    pkv.paged_attn_prefill_q4(q, p.cache, i32([0, 100, 110, 140]), i32([0, 300, 800, 840]), i32(p.tables), SCALE, 30,
+                              500, out=out)  # the first has more rows than stated
+    assert pkv.device_error() == ["LEN_RANGE"]
+    assert (out[:100] == 5).all() and (out[100:] != 5).any(-1).all()
+    bad = p.tables.copy()
+    bad[1, 0] = -9
+    pkv.paged_attn_prefill_q4(q, p.cache, i32([0, 100, 110, 140]), i32([0, 300, 800, 840]), i32(bad), SCALE, 100, 500,
+                              out=out)
+    assert pkv.device_error() == ["BLOCK_RANGE"]
+
+
+def test_prefill_last_row_equals_decode():
+    """The last row of a prompt and the decode of the same token agree within their allowances."""
+    p, q, out = prefill_case([(777, 700)], 16, 8, seed=2)
+    d = pkv.paged_attn_decode_q4(q[-1:].to(dev()), p.cache, i32([777]), i32(p.tables), SCALE)
+    ref, tol = q4_ref.attention(q[-1:].double(), p.held[0][0], p.held[0][1], SCALE, 777)
+    q4_ref.check(d, ref, tol, "decode")
+    assert (np.abs(d.double().cpu().numpy() - out[-1:].double().cpu().numpy()) <= 2 * tol).all()
+
+
+def test_binding_refusals():
+    p = Pool([300], 2, 7)
+    q = queries(1, 4, 3).to(dev())
+    with pytest.raises(ValueError):
+        pkv.paged_attn_decode_q4(q, p.cache, i32([300, 1]), i32(p.tables), SCALE)
+    with pytest.raises(ValueError):
+        pkv.paged_attn_decode_q4(q[..., :64], p.cache, i32([300]), i32(p.tables), SCALE)
+    with pytest.raises(pkv.PkvError):
+        pkv.paged_attn_decode_q4(q, p.cache, i32([300]), i32(p.tables), SCALE,
+                                 workspace=torch.empty(16, dtype=torch.uint8, device=dev()))
+    with pytest.raises(pkv.PkvError):
+        pkv.paged_attn_decode_q4(q[:, :3].contiguous(), p.cache, i32([300]), i32(p.tables), SCALE)
+    with pytest.raises(ValueError):
+        pkv.paged_attn_prefill_q4(q, p.cache, i32([0, 1]), i32([0, 1, 2]), i32(p.tables), SCALE, 1, 1)

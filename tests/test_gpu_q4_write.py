@@ -1,0 +1,126 @@
+"""4-bit cache write and read-back on the GPU: held values exactly the
+reference's, every other slot untouched."""
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_304_gb300 as pkv
+from tests import q4_ref
+from tests.gpu_util import dev, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(n, h, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((n, h, 128), generator=g)
+    x[..., 3::29] *= 9
+    return x.to(torch.bfloat16)
+
+
+def check_write(k, v, slots, hkv, ts=(1.0, 1.0), nb=3, dk=None, dv=None):
+    g = torch.Generator().manual_seed(9)
+    d = torch.randint(0, 256, (2, nb, 256, hkv, 64), generator=g, dtype=torch.uint8)
+    s = torch.randint(0, 120, (2, nb, 256, hkv, 8), generator=g, dtype=torch.uint8)
+    dd, ds = d.to(dev()), s.to(dev())
+    c = pkv.Q4Cache(dd[0], ds[0], dd[1], ds[1], *ts)
+    pkv.device_error(clear=True)
+    pkv.kv_cache_write_q4(k.to(dev()) if dk is None else dk, v.to(dev()) if dv is None else dv, i32(slots), c)
+    assert pkv.device_error() == []
+    for kv, x in enumerate((k, v)):
+        ref = q4_ref.values(d[kv].view(-1, hkv, 64), s[kv].view(-1, hkv, 8), ts[kv])
+        data, scales = q4_ref.quantise(x, ts[kv])
+        for i, slot in enumerate(slots):
+            if slot >= 0:
+                ref[slot] = q4_ref.values(data[i], scales[i], ts[kv])
+        got = q4_ref.values(dd[kv].cpu().view(-1, hkv, 64), ds[kv].cpu().view(-1, hkv, 8), ts[kv])
+        assert np.array_equal(got, ref, equal_nan=True)
+    # read-back: the held values rounded once to bf16 (fp32 product of an exact
+    # value with the tensor scale, then bf16: at most one bf16 step where the
+    # two roundings meet a tie, none for a power of two)
+    ko, vo = pkv.kv_cache_read_q4(c, i32(slots))
+    for kv, o in enumerate((ko, vo)):
+        held = q4_ref.values(dd[kv].cpu().view(-1, hkv, 64), ds[kv].cpu().view(-1, hkv, 8), ts[kv])
+        exp = np.where(np.asarray(slots)[:, None, None] >= 0, held[np.maximum(slots, 0)], 0.0)
+        f32 = torch.from_numpy(exp.astype(np.float32)).to(torch.bfloat16)
+        assert torch.equal(o.cpu().nan_to_num(nan=12345.0), f32.nan_to_num(nan=12345.0))
+    return c
+
+
+@pytest.mark.parametrize("hkv", [1, 3, 8])
+@pytest.mark.parametrize("n", [1, 5, 300])
+@pytest.mark.parametrize("ts", [(1.0, 1.0), (0.25, 3.7)])
+def test_write_matches_reference(n, hkv, ts):
+    slots = np.random.default_rng(n + hkv).permutation(3 * 256)[:n].astype(np.int32)
+    slots[1::4] = -1
+    check_write(rows(n, hkv, 1), rows(n, hkv, 2), slots, hkv, ts)
+
+
+def test_ties_and_special_values():
+    """Exact ties between codes at every scale's mantissa, infinities, NaN, zeros and tiny groups."""
+    x = torch.zeros(40, 2, 128)
+    for m in range(8):  # scales 1.m/8 * 2^e: the group's largest is 6 * scale
+        s = (1 + m / 8) * 2.0 ** (m - 4)
+        t = torch.tensor([6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, -0.25, -0.75, -1.25, -1.75, -2.5, -3.5, -5, -0.0])
+        x[m, :, :] = (t * s).repeat(8)
+    x[8, 0, 5] = float("inf")
+    x[9, 1, 17] = float("nan")
+    x[10, 0, 100] = float("-inf")
+    x[10, 0, 101] = float("nan")
+    x[11] = 1e-30
+    x[12] = 3e38
+    x[13, 0] = 6 * 2.0**-10          # on the tie between scale 0 and 2^-9: the even one is 0
+    x[14, 0] = 6.05 * 2.0**-10       # just above: the smallest scale
+    x[15, :, ::2] = -1.0
+    for i in range(16, 40):          # scale ties: largest = 6 * (1 + (2j+1)/16)
+        x[i] = 6 * (1 + (2 * (i - 16) + 1) / 16) * torch.linspace(-1, 1, 128)
+    k = x.to(torch.bfloat16)
+    check_write(k, k.flip(0), np.arange(40, dtype=np.int32) * 17 % 700, 2)
+
+
+def test_strided_rows_of_a_fused_projection():
+    n, hkv = 70, 4
+    buf = rows(n, 3 * hkv, 3)
+    db = buf.to(dev())
+    slots = np.arange(n, dtype=np.int32)[::-1].copy()
+    check_write(buf[:, hkv:2 * hkv], buf[:, 2 * hkv:], slots, hkv, dk=db[:, hkv:2 * hkv], dv=db[:, 2 * hkv:])
+
+
+def test_out_of_range_slots_flag_and_skip():
+    c = pkv.Q4Cache.empty(2, 8, dev())
+    k = rows(3, 8).to(dev())
+    pkv.device_error(clear=True)
+    pkv.kv_cache_write_q4(k, k, i32([512, -2, 7]), c)
+    assert pkv.device_error() == ["SLOT_RANGE"]
+    assert int((c.k_scales != 0).any(-1).any(-1).sum()) == 1
+    ko, _ = pkv.kv_cache_read_q4(c, i32([7, 512, -1, -5]))
+    assert pkv.device_error() == ["SLOT_RANGE"]
+    assert (ko[1:] == 0).all() and (ko[0] != 0).any()
+
+
+def test_no_tokens_and_float8_scales():
+    d = torch.zeros((2, 2, 256, 8, 64), dtype=torch.uint8, device=dev())
+    s = torch.zeros((2, 2, 256, 8, 8), dtype=torch.float8_e4m3fn, device=dev())
+    c = pkv.Q4Cache(d[0], s[0], d[1], s[1])
+    e = torch.empty((0, 8, 128), dtype=torch.bfloat16, device=dev())
+    pkv.kv_cache_write_q4(e, e, i32([]), c)
+    ko, vo = pkv.kv_cache_read_q4(c, i32([]))
+    assert ko.shape == vo.shape == (0, 8, 128)
+
+
+def test_binding_refusals():
+    c = pkv.Q4Cache.empty(2, 8, dev())
+    k = rows(3, 8).to(dev())
+    with pytest.raises(ValueError):
+        pkv.kv_cache_write_q4(k, k, i32([1, 2]), c)
+    with pytest.raises(ValueError):
+        pkv.kv_cache_write_q4(k[:, :4], k, i32([1, 2, 3]), c)
+    with pytest.raises(ValueError):
+        pkv.kv_cache_write_q4(k, k.transpose(0, 1).contiguous().transpose(0, 1), i32([1, 2, 3]), c)
+    with pytest.raises(TypeError):
+        pkv.kv_cache_write_q4(k.float(), k, i32([1, 2, 3]), c)
+    with pytest.raises(ValueError):
+        pkv.Q4Cache(c.k_data, c.k_scales[:1], c.v_data, c.v_scales)
+    with pytest.raises(ValueError):
+        pkv.Q4Cache(c.k_data, c.k_scales, c.v_data, c.v_scales, k_scale=0.0)
