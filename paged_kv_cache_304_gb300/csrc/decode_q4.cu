@@ -1,5 +1,40 @@
-// decode_q4.cu -- one query token per sequence against the 4-bit cache (first,
-// plain form: a warp per query head walks the context one key at a time).
+// decode_q4.cu -- one query token per sequence against the 4-bit cache.
+//
+// Bound by HBM: a context token costs 144 bytes per kv head (codes and scales of
+// its K and V rows), 3.6 times less than in bf16, so the arithmetic that turns
+// codes into matrix operands has to fit into a quarter of the time that the
+// bf16 kernel has.
+//
+// * Work split.  The sequences' tiles of T = 16 R tokens are laid end to end and
+//   every CTA takes an equal share of the tiles (persistent CTAs, one to three
+//   per SM).  Sequences that straddle CTAs leave partial (max, sum, output)
+//   triples that a combine kernel merges.
+// * Pipeline.  A producer warp fetches a tile's K and V codes for all kv heads
+//   with one TMA tensor copy each ([head][token][64 bytes], 64-byte swizzle) and
+//   the scales, which are contiguous, with plain bulk copies, into a ring.
+// * Operands.  Warp (h, r) computes kv head h for tokens 16r .. 16r+15 of a
+//   tile.  The tokens are the rows of S^T = K Q^T (m16n8k16, fp16 in, fp32
+//   out; the group's query heads are the 8 columns) and then the inner dimension
+//   of O^T = V^T P^T, so a group of up to 8 query heads wastes no matrix work on
+//   empty rows.  The order of dims in the first product and of tokens in the
+//   second is free as long as both operands agree:
+//     - a lane takes 32 consecutive dims of its two K rows (one 16-byte load,
+//       two scales a row) and the same 32 dims of its query head;
+//     - for V a lane takes group g of 16 dims of four tokens (8-byte loads, one
+//       scale a token), and exchanges nibbles between two tokens' words, so that
+//       a byte holds the same dim of both: the pair that the operand wants.
+//   Lane g's row of S^T is token tau(g); tau spreads the rows so that both kinds
+//   of load are free of bank conflicts under the 64-byte swizzle.
+//   A byte of two codes becomes two fp16 values in one conversion and one
+//   multiplication by the scale (exact).  The query is scaled by a power of two
+//   per head (its largest element to 2^14 .. 2^15), undone in the softmax scale.
+// * Softmax in log2 units.  The running maximum is raised only when a score
+//   exceeds it by 8 (p <= 2^8 is in range of fp16), which costs a vote per tile
+//   instead of a reduction; P^T is the transpose of S^T's fragment (movmatrix).
+// * Slots behind a sequence's end hold anything: their scores are masked and
+//   their V scales are taken as zero (a stale scale may be NaN).
+// * Waits are bounded: a wait that exceeds two seconds sets
+//   PKV_DEVERR_WAIT_TIMEOUT and the CTA returns.
 #include <cuda_runtime.h>
 
 #include "pkv_device.cuh"
@@ -11,107 +46,707 @@ namespace {
 
 __device__ unsigned int g_err_decode_q4;
 
-struct Acc {
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+constexpr int kMaxStages = 6;
+constexpr int kQSlots = 2;      // query staging slots (one per unit in flight)
+constexpr int kMinTokens = 64;  // smallest share of a CTA
+constexpr int kMaxHeadWarps = 16;
+constexpr size_t kSmemMax = 232448;
+
+enum : int32_t { kFirst = 1, kLast = 2, kWhole = 4 };
+
+struct alignas(16) TileHeader {
+  int32_t b;      // sequence, or -1 for "no more work"
+  int32_t hi;     // the unit ends before token hi
+  int32_t t0;     // first token of this tile
+  int32_t flags;  // kFirst / kLast tile of the unit; kWhole: unit == sequence
+  int32_t slot;   // partial-result slot of the unit (b + CTA index)
+  int32_t pad[3];
 };
+
+struct Params {
+  const uint16_t* q;
+  const int32_t* ctx;
+  const int32_t* tables;
+  uint16_t* out;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  float* ws_o;    // [slots, Hq, 128] unnormalised partial outputs
+  float2* ws_ml;  // [slots, Hq] (row max in log2 units, row sum)
+  int2* ws_meta;  // [B] first and last CTA holding sequence b
+  int32_t maxb, B, Hq, Hkv, G, num_blocks, lmax;
+  int32_t log2_r, tile, log2_tile, stages;  // R, T and the ring's depth
+  float sl2;      // scale * k_scale * log2(e)
+  float v_scale;
+  uint32_t data_bytes, scale_bytes, stage_bytes, q_slot_bytes;
+};
+
+__device__ __forceinline__ int clamp_len(int L, int lmax) {
+  if (L < 0 || L > lmax) {
+    atomicOr(&g_err_decode_q4, PKV_DEVERR_LEN_RANGE);
+    L = L < 0 ? 0 : lmax;
+  }
+  return L;
+}
+
+struct Smem {
+  uint8_t* stages;
+  uint8_t* qbuf;
+  float* ex_o;     // [warp][value][lane]: a warp's output at a unit's end
+  float2* ex_ml;   // [warp][head of the group]
+  TileHeader* hdr;
+  uint64_t *full, *empty, *qfull, *qempty, *xfull, *xempty;
+};
+
+// One warp's exchange area: 32 values per lane and 8 (max, sum) pairs for every
+// eight query heads.
+__host__ __device__ constexpr uint32_t exchange_bytes(int nt) { return nt * (32 * 32 * 4 + 8 * 8); }
+
+__device__ __forceinline__ Smem carve(uint8_t* base, const Params& p, int nt) {
+  Smem s;
+  const int warps = p.Hkv << p.log2_r;
+  s.stages = base;
+  s.qbuf = base + p.stages * p.stage_bytes;
+  s.ex_o = reinterpret_cast<float*>(s.qbuf + kQSlots * p.q_slot_bytes);
+  uint8_t* after = reinterpret_cast<uint8_t*>(s.ex_o);
+  if (p.log2_r) after += warps * nt * 32 * 32 * 4;
+  s.ex_ml = reinterpret_cast<float2*>(after);
+  if (p.log2_r) after += warps * nt * 64;
+  s.hdr = reinterpret_cast<TileHeader*>(after);
+  s.full = reinterpret_cast<uint64_t*>(s.hdr + kMaxStages);
+  s.empty = s.full + kMaxStages;
+  s.qfull = s.empty + kMaxStages;
+  s.qempty = s.qfull + kQSlots;
+  s.xfull = s.qempty + kQSlots;
+  s.xempty = s.xfull + kMaxKvHeads;
+  return s;
+}
+constexpr size_t kFixedBytes =
+    1024 + kMaxStages * sizeof(TileHeader) + (2 * kMaxStages + 2 * kQSlots + 2 * kMaxKvHeads) * sizeof(uint64_t);
+
+// Used only after a timeout: lets copies already issued land before the shared
+// memory is given up (bounded, 100 ms; the timeout has been reported).
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > 100000000ull) return;
+}
+
+// ------------------------------------------------------------------ producer
+struct ProducerState {
+  uint32_t it = 0, stage = 0, phase = 0;  // tiles issued, ring position
+  uint32_t units = 0;
+  bool ok = true;
+};
+
+__device__ __forceinline__ int load_block(const Params& p, int b, int lb) {
+  int phys = __ldg(p.tables + static_cast<int64_t>(b) * p.maxb + lb);
+  if (phys < 0 || phys >= p.num_blocks) {
+    atomicOr(&g_err_decode_q4, PKV_DEVERR_BLOCK_RANGE);
+    phys = 0;
+  }
+  return phys;
+}
+
+// Issue every tile of unit (b, [lo, hi)), lo a multiple of the tile.  Lane 0 of
+// the producer warp only.
+__device__ void emit_unit(const Params& p, const Smem& sm, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                          ProducerState& ps, int b, int lo, int hi, int L, int first_phys) {
+  int lb_cur = -1, phys = 0, nxt = first_phys;
+  for (int t = lo; t < hi; t += p.tile) {
+    const int lb = t / kBlockSize;
+    if (lb != lb_cur) {
+      phys = nxt;
+      lb_cur = lb;
+      if ((lb + 1) * kBlockSize < hi) nxt = load_block(p, b, lb + 1);
+    }
+    const uint32_t st = ps.stage;
+    if (!mbar_wait(&sm.empty[st], ps.phase ^ 1u, &g_err_decode_q4)) {
+      ps.ok = false;
+      return;
+    }
+    TileHeader h;
+    h.b = b;
+    h.hi = hi;
+    h.t0 = t;
+    h.flags = (t == lo ? kFirst : 0) | (t + p.tile >= hi ? kLast : 0) | (lo == 0 && hi == L ? kWhole : 0);
+    h.slot = b + blockIdx.x;
+    h.pad[0] = h.pad[1] = h.pad[2] = 0;
+    sm.hdr[st] = h;
+    if (h.flags & kFirst) {
+      const uint32_t qs = ps.units % kQSlots;
+      if (!mbar_wait(&sm.qempty[qs], ((ps.units / kQSlots) & 1u) ^ 1u, &g_err_decode_q4)) {
+        ps.ok = false;
+        return;
+      }
+      const uint32_t qbytes = static_cast<uint32_t>(p.Hq) * kHeadDim * 2;
+      mbar_arrive_expect_tx(&sm.qfull[qs], qbytes);
+      bulk_g2s(sm.qbuf + qs * p.q_slot_bytes, p.q + static_cast<int64_t>(b) * p.Hq * kHeadDim, qbytes,
+               &sm.qfull[qs]);
+      ++ps.units;
+    }
+    uint8_t* dst = sm.stages + st * p.stage_bytes;
+    mbar_arrive_expect_tx(&sm.full[st], 2 * (p.data_bytes + p.scale_bytes));
+    const int tin = t & (kBlockSize - 1);
+    const int64_t row = (static_cast<int64_t>(phys) * kBlockSize + tin) * p.Hkv * q4::kRowScales;
+    tma_load_4d(dst, kmap, &sm.full[st], 0, tin, 0, phys);
+    bulk_g2s(dst + 2 * p.data_bytes, p.k_scales + row, p.scale_bytes, &sm.full[st]);
+    tma_load_4d(dst + p.data_bytes, vmap, &sm.full[st], 0, tin, 0, phys);
+    bulk_g2s(dst + 2 * p.data_bytes + p.scale_bytes, p.v_scales + row, p.scale_bytes, &sm.full[st]);
+    ++ps.it;
+    if (++ps.stage == static_cast<uint32_t>(p.stages)) {
+      ps.stage = 0;
+      ps.phase ^= 1u;
+    }
+  }
+}
+
+__device__ __forceinline__ int warp_incl_scan(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+__device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kmap, const CUtensorMap* vmap) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) {
+    prefetch_tensormap(kmap);
+    prefetch_tensormap(vmap);
+  }
+  const int round = p.tile - 1;
+  long long total = 0;  // tiles of the batch
+  for (int base = 0; base < p.B; base += 32) {
+    const int b = base + lane;
+    const int L = b < p.B ? clamp_len(__ldg(p.ctx + b), p.lmax) : 0;
+    total += __reduce_add_sync(0xffffffffu, static_cast<unsigned>((L + round) >> p.log2_tile));
+  }
+  ProducerState ps;
+  if (total > 0) {
+    long long per = (total + gridDim.x - 1) / gridDim.x;
+    const int least = max(1, kMinTokens >> p.log2_tile);
+    if (per < least) per = least;
+    const long long my_lo = static_cast<long long>(blockIdx.x) * per;
+    const long long my_hi = my_lo + per < total ? my_lo + per : total;
+    long long S = 0;
+    for (int base = 0; base < p.B && S < my_hi && ps.ok; base += 32) {
+      const int b = base + lane;
+      const int L = b < p.B ? clamp_len(__ldg(p.ctx + b), p.lmax) : 0;
+      const int n = (L + round) >> p.log2_tile;
+      const int incl = warp_incl_scan(n, lane);
+      const long long Sb = S + incl - n;
+      if (n > 0 && Sb / per == blockIdx.x)
+        p.ws_meta[b] = make_int2(static_cast<int>(Sb / per), static_cast<int>((Sb + n - 1) / per));
+      const long long lo = my_lo > Sb ? my_lo : Sb;
+      const long long hi = my_hi < Sb + n ? my_hi : Sb + n;
+      const bool has = n > 0 && lo < hi;
+      unsigned mask = __ballot_sync(0xffffffffu, has);
+      const int lo_t = has ? static_cast<int>(lo - Sb) << p.log2_tile : 0;
+      const int hi_t = has ? min(L, static_cast<int>(hi - Sb) << p.log2_tile) : 0;
+      const int first_phys = has ? load_block(p, b, lo_t / kBlockSize) : 0;  // of every piece together
+      while (mask) {
+        const int j = __ffs(mask) - 1;
+        mask &= mask - 1;
+        const int bj = __shfl_sync(0xffffffffu, b, j);
+        const int loj = __shfl_sync(0xffffffffu, lo_t, j);
+        const int hij = __shfl_sync(0xffffffffu, hi_t, j);
+        const int Lj = __shfl_sync(0xffffffffu, L, j);
+        const int physj = __shfl_sync(0xffffffffu, first_phys, j);
+        if (lane == 0 && ps.ok) emit_unit(p, sm, kmap, vmap, ps, bj, loj, hij, Lj, physj);
+        ps.ok = __shfl_sync(0xffffffffu, ps.ok, 0);
+      }
+      S += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  if (lane == 0 && ps.ok) {
+    if (mbar_wait(&sm.empty[ps.stage], ps.phase ^ 1u, &g_err_decode_q4)) {
+      sm.hdr[ps.stage].b = -1;
+      mbar_arrive(&sm.full[ps.stage]);
+    }
+  }
+  if (lane == 0 && !ps.ok) {
+    const uint32_t n = p.stages;
+    for (uint32_t i = ps.it > n ? ps.it - n : 0; i < ps.it; ++i) drain_wait(&sm.full[i % n], (i / n) & 1u);
+    for (uint32_t u = ps.units > kQSlots ? ps.units - kQSlots : 0; u < ps.units; ++u)
+      drain_wait(&sm.qfull[u % kQSlots], (u / kQSlots) & 1u);
+  }
+}
+
+// ------------------------------------------------------------------ consumer
+__device__ __forceinline__ uint32_t dup_lo(uint32_t h2) { return __byte_perm(h2, 0, 0x1010); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t h2) { return __byte_perm(h2, 0, 0x3232); }
+
+// NT: eights of query heads of a group (1 or 2).
+template <int NT>
+__device__ void consumer(const Params& p, const Smem& sm) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int R = 1 << p.log2_r;
+  const int h = w >> p.log2_r, r = w & (R - 1);
+  const int g = lane >> 2, c = lane & 3;
+  // tau(2i) = (i & 1) | (i & 2) << 1, tau(2i + 1) = tau(2i) ^ 3, tau(m + 8) = tau(m) + 8
+  const int tg = ((((g >> 1) & 1) | ((g >> 2) << 2)) ^ ((g & 1) ? 3 : 0));
+  const int ta = (c & 1) | ((c >> 1) << 2), tb = ta ^ 3;
+  const uint32_t head_row = static_cast<uint32_t>(h * p.tile + 16 * r) * q4::kRowBytes;
+  const uint32_t koff = head_row + tg * q4::kRowBytes + ((c ^ ((tg >> 1) & 3)) << 4);
+  const uint32_t va = p.data_bytes + head_row + ta * q4::kRowBytes + (((g >> 1) ^ ((ta >> 1) & 3)) << 4) + (g & 1) * 8;
+  const uint32_t vb = p.data_bytes + head_row + tb * q4::kRowBytes + (((g >> 1) ^ ((tb >> 1) & 3)) << 4) + (g & 1) * 8;
+  const uint32_t srow = static_cast<uint32_t>(p.Hkv) * q4::kRowScales;  // scale bytes of a token
+  const uint32_t ksoff = 2 * p.data_bytes + (16 * r + tg) * srow + h * q4::kRowScales + 2 * c;
+  const uint32_t vsoff = 2 * p.data_bytes + p.scale_bytes + 16 * r * srow + h * q4::kRowScales + g;
+  const uint32_t vsa = vsoff + ta * srow, vsb = vsoff + tb * srow;
+  const float NEG_INF = -INFINITY;
+
+  uint32_t qb[NT][16];   // B operand of the first product: this lane's 32 dims of query head g (+ 8)
+  float acc[NT][8][4];   // O^T: dims 16g + 2i (0, 1) and 16g + 2i + 1 (2, 3) of heads 2c, 2c + 1
+  float sl[NT][2], m[NT][2], l[NT][2];
+  uint32_t stage = 0, phase = 0, units = 0;
+  const uint32_t ring = smem_u32(sm.stages);
+
+  for (;;) {
+    if (!mbar_wait(&sm.full[stage], phase, &g_err_decode_q4)) return;
+    const TileHeader hd = sm.hdr[stage];
+    if (hd.b < 0) return;
+    if (hd.flags & kFirst) {
+      const uint32_t qs = units % kQSlots;
+      if (!mbar_wait(&sm.qfull[qs], (units / kQSlots) & 1u, &g_err_decode_q4)) return;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float x[32];
+        float top = 0.f;
+        if (g + 8 * n < p.G) {
+          const uint4* src = reinterpret_cast<const uint4*>(sm.qbuf + qs * p.q_slot_bytes +
+                                                            (h * p.G + g + 8 * n) * (kHeadDim * 2) + c * 64);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 a = src[i];
+            const uint32_t ww[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              x[8 * i + 2 * j] = q4::bf_lo(ww[j]);
+              x[8 * i + 2 * j + 1] = q4::bf_hi(ww[j]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^(14 - e) for a largest element in [2^e, 2^(e+1))
+        const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 15), 254);
+        const float f = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+        const float inv = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) qb[n][j] = pack_f16x2(x[2 * j] * f, x[2 * j + 1] * f);
+        sl[n][0] = p.sl2 * __shfl_sync(0xffffffffu, inv, 8 * c);
+        sl[n][1] = p.sl2 * __shfl_sync(0xffffffffu, inv, 8 * c + 4);
+        m[n][0] = m[n][1] = NEG_INF;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.qempty[qs]);
+    }
+    const int t0 = hd.t0 + 16 * r;
+    if (t0 < hd.hi) {
+      const uint32_t sb = ring + stage * p.stage_bytes;
+      const uint4 k0 = lds128(sb + koff), k1 = lds128(sb + koff + 8 * q4::kRowBytes);
+      const uint32_t ks0 = lds_u16(sb + ksoff), ks1 = lds_u16(sb + ksoff + 8 * srow);
+      const uint2 v0 = lds64(sb + va), v1 = lds64(sb + vb);
+      const uint2 v2 = lds64(sb + va + 8 * q4::kRowBytes), v3 = lds64(sb + vb + 8 * q4::kRowBytes);
+      uint32_t s0 = lds_u8(sb + vsa), s1 = lds_u8(sb + vsb);
+      uint32_t s2 = lds_u8(sb + vsa + 8 * srow), s3 = lds_u8(sb + vsb + 8 * srow);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[stage]);
+
+      // S^T = K Q^T in two chains of four k-steps
+      float sa[NT][4], sc[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sa[n][i] = sc[n][i] = 0.f;
+      {
+        const uint32_t f0 = q4::dec_scale2(ks0), f1 = q4::dec_scale2(ks1);
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t e0 = i < 2 ? dup_lo(f0) : dup_hi(f0), e1 = i < 2 ? dup_lo(f1) : dup_hi(f1);
+          uint32_t a[4], b[4];
+          q4::dec8(w0[i], a);
+          q4::dec8(w1[i], b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            a[j] = q4::hmul2(a[j], e0);
+            b[j] = q4::hmul2(b[j], e1);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16_16816(sa[n], a[0], b[0], a[1], b[1], qb[n][4 * i], qb[n][4 * i + 1]);
+            mma_f16_16816(sc[n], a[2], b[2], a[3], b[3], qb[n][4 * i + 2], qb[n][4 * i + 3]);
+          }
+        }
+      }
+      const int left = hd.hi - t0;  // real tokens of the sixteen
+      const bool ragged = left < 16;
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float x0 = (sa[n][0] + sc[n][0]) * sl[n][0], x1 = (sa[n][1] + sc[n][1]) * sl[n][1];
+        float x2 = (sa[n][2] + sc[n][2]) * sl[n][0], x3 = (sa[n][3] + sc[n][3]) * sl[n][1];
+        if (ragged) {
+          if (tg >= left) x0 = x1 = NEG_INF;
+          if (tg + 8 >= left) x2 = x3 = NEG_INF;
+        }
+        const float y0 = fmaxf(x0, x2), y1 = fmaxf(x1, x3);
+        if (__any_sync(0xffffffffu, y0 > m[n][0] + 8.f || y1 > m[n][1] + 8.f)) {
+          float n0 = y0, n1 = y1;
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
+            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
+          }
+          n0 = fmaxf(n0, m[n][0]);
+          n1 = fmaxf(n1, m[n][1]);
+          // a head of the group beyond its size, or none seen yet: -inf stays, factor 1
+          const float a0 = n0 == NEG_INF ? 1.f : fast_exp2(m[n][0] - n0);
+          const float a1 = n1 == NEG_INF ? 1.f : fast_exp2(m[n][1] - n1);
+          m[n][0] = n0;
+          m[n][1] = n1;
+          l[n][0] *= a0;
+          l[n][1] *= a1;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[n][i][0] *= a0;
+            acc[n][i][1] *= a1;
+            acc[n][i][2] *= a0;
+            acc[n][i][3] *= a1;
+          }
+        }
+        const float u0 = m[n][0] == NEG_INF ? 0.f : m[n][0], u1 = m[n][1] == NEG_INF ? 0.f : m[n][1];
+        const float p0 = fast_exp2(x0 - u0), p1 = fast_exp2(x1 - u1), p2 = fast_exp2(x2 - u0), p3 = fast_exp2(x3 - u1);
+        l[n][0] += p0 + p2;
+        l[n][1] += p1 + p3;
+        pb[n][0] = movmatrix_trans(pack_f16x2(p0, p1));
+        pb[n][1] = movmatrix_trans(pack_f16x2(p2, p3));
+      }
+      // O^T += V^T P^T
+      if (ragged) {
+        if (ta >= left) s0 = 0;
+        if (tb >= left) s1 = 0;
+        if (ta + 8 >= left) s2 = 0;
+        if (tb + 8 >= left) s3 = 0;
+      }
+      const uint32_t e01 = q4::dec_scale2(s0 | s1 << 8), e23 = q4::dec_scale2(s2 | s3 << 8);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t a0 = half ? v0.y : v0.x, a1 = half ? v1.y : v1.x;
+        const uint32_t a2 = half ? v2.y : v2.x, a3 = half ? v3.y : v3.x;
+        const uint32_t kLow = 0x0f0f0f0fu;
+        uint32_t ev0[4], od0[4], ev1[4], od1[4];
+        q4::dec8((a0 & kLow) | ((a1 << 4) & ~kLow), ev0);
+        q4::dec8(((a0 >> 4) & kLow) | (a1 & ~kLow), od0);
+        q4::dec8((a2 & kLow) | ((a3 << 4) & ~kLow), ev1);
+        q4::dec8(((a2 >> 4) & kLow) | (a3 & ~kLow), od1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t f0 = q4::hmul2(ev0[i], e01), f1 = q4::hmul2(od0[i], e01);
+          const uint32_t f2 = q4::hmul2(ev1[i], e23), f3 = q4::hmul2(od1[i], e23);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16_16816(acc[n][4 * half + i], f0, f1, f2, f3, pb[n][0], pb[n][1]);
+        }
+      }
+    } else {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[stage]);
+    }
+
+    if (hd.flags & kLast) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], o);
+      // Merge the R warps of the head through shared memory: each then owns the
+      // dims 16g + 2i of i in [8r / R, 8(r + 1) / R).
+      const int i0 = (8 * r) >> p.log2_r, i1 = (8 * (r + 1)) >> p.log2_r;
+      float* ex = sm.ex_o + static_cast<size_t>(h << p.log2_r) * (NT * 1024);
+      float2* eml = sm.ex_ml + (h << p.log2_r) * (NT * 8);
+      if (p.log2_r) {
+        if (!mbar_wait(&sm.xempty[h], (units & 1u) ^ 1u, &g_err_decode_q4)) return;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ex[((r * NT + n) * 32 + i * 4 + k) * 32 + lane] = acc[n][i][k];
+          if (g == 0) {
+            eml[(r * NT + n) * 8 + 2 * c] = make_float2(m[n][0], l[n][0]);
+            eml[(r * NT + n) * 8 + 2 * c + 1] = make_float2(m[n][1], l[n][1]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.xfull[h]);
+        if (!mbar_wait(&sm.xfull[h], units & 1u, &g_err_decode_q4)) return;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float M0 = m[n][0], M1 = m[n][1], L0 = l[n][0], L1 = l[n][1];
+        float w0[4], w1[4];  // weights of the R <= 4 warps
+        if (p.log2_r) {
+          M0 = M1 = NEG_INF;
+          L0 = L1 = 0.f;
+          for (int rr = 0; rr < R; ++rr) {
+            M0 = fmaxf(M0, eml[(rr * NT + n) * 8 + 2 * c].x);
+            M1 = fmaxf(M1, eml[(rr * NT + n) * 8 + 2 * c + 1].x);
+          }
+          const float u0 = M0 == NEG_INF ? 0.f : M0, u1 = M1 == NEG_INF ? 0.f : M1;
+#pragma unroll
+          for (int rr = 0; rr < 4; ++rr) {
+            if (rr < R) {
+              const float2 e0 = eml[(rr * NT + n) * 8 + 2 * c], e1 = eml[(rr * NT + n) * 8 + 2 * c + 1];
+              w0[rr] = fast_exp2(e0.x - u0);
+              w1[rr] = fast_exp2(e1.x - u1);
+              L0 += w0[rr] * e0.y;
+              L1 += w1[rr] * e1.y;
+            }
+          }
+        }
+        const int q0 = 8 * n + 2 * c;  // head of the group
+        const bool ok0 = q0 < p.G, ok1 = q0 + 1 < p.G;
+        const float inv0 = (hd.flags & kWhole) ? p.v_scale / L0 : 1.f, inv1 = (hd.flags & kWhole) ? p.v_scale / L1 : 1.f;
+        const int64_t row = (static_cast<int64_t>(hd.flags & kWhole ? hd.b : hd.slot) * p.Hq + h * p.G + q0) * kHeadDim + 16 * g;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i < i0 || i >= i1) continue;
+          float o[4] = {acc[n][i][0], acc[n][i][1], acc[n][i][2], acc[n][i][3]};
+          if (p.log2_r) {
+            o[0] = o[1] = o[2] = o[3] = 0.f;
+#pragma unroll
+            for (int rr = 0; rr < 4; ++rr) {
+              if (rr < R) {
+                const float* e = ex + ((rr * NT + n) * 32 + i * 4) * 32 + lane;
+                o[0] = fmaf(w0[rr], e[0], o[0]);
+                o[1] = fmaf(w1[rr], e[32], o[1]);
+                o[2] = fmaf(w0[rr], e[64], o[2]);
+                o[3] = fmaf(w1[rr], e[96], o[3]);
+              }
+            }
+          }
+          if (hd.flags & kWhole) {
+            if (ok0) *reinterpret_cast<uint32_t*>(p.out + row + 2 * i) = pack_bf16x2(o[0] * inv0, o[2] * inv0);
+            if (ok1) *reinterpret_cast<uint32_t*>(p.out + row + kHeadDim + 2 * i) = pack_bf16x2(o[1] * inv1, o[3] * inv1);
+          } else {
+            if (ok0) *reinterpret_cast<float2*>(p.ws_o + row + 2 * i) = make_float2(o[0], o[2]);
+            if (ok1) *reinterpret_cast<float2*>(p.ws_o + row + kHeadDim + 2 * i) = make_float2(o[1], o[3]);
+          }
+        }
+        if (!(hd.flags & kWhole) && r == 0 && g == 0) {
+          float2* ml = p.ws_ml + static_cast<int64_t>(hd.slot) * p.Hq + h * p.G + q0;
+          if (ok0) ml[0] = make_float2(M0, L0);
+          if (ok1) ml[1] = make_float2(M1, L1);
+        }
+      }
+      if (p.log2_r) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.xempty[h]);
+      }
+      ++units;
+    }
+    if (++stage == static_cast<uint32_t>(p.stages)) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(NT == 1 ? 32 * (kMaxHeadWarps + 1) : 32 * (kMaxHeadWarps / 2 + 1))
+    decode_q4_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  const Smem sm = carve(base, p, NT);
+  const int warp = threadIdx.x >> 5, warps = p.Hkv << p.log2_r;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], warps);
+    }
+    for (int s = 0; s < kQSlots; ++s) {
+      mbar_init(&sm.qfull[s], 1);
+      mbar_init(&sm.qempty[s], warps);
+    }
+    for (int s = 0; s < p.Hkv; ++s) {
+      mbar_init(&sm.xfull[s], 1 << p.log2_r);
+      mbar_init(&sm.xempty[s], 1 << p.log2_r);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (warp == warps)
+    producer(p, sm, &kmap, &vmap);
+  else
+    consumer<NT>(p, sm);
+}
+
+// Merge the partials of sequences that straddle CTAs; zero pad rows.  One warp
+// per (sequence, query head), lane i dims 4i .. 4i+3; the lanes share the pass
+// over the partials' maxima and sums.
+constexpr int kCombineWarps = 4;
+
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_q4_kernel(const Params p, int grid) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t pair = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
+  if (pair >= static_cast<int64_t>(p.B) * p.Hq) return;
+  const int b = static_cast<int>(pair / p.Hq), hq = static_cast<int>(pair - static_cast<int64_t>(b) * p.Hq);
+  const int lane = threadIdx.x & 31;
+  const int L_in = __ldg(p.ctx + b);
+  const int2 meta = p.ws_meta[b];  // read only when the length is positive, i.e. when it was written
+  const int L = clamp_len(L_in, p.lmax);
+  uint16_t* o = p.out + pair * kHeadDim + 4 * lane;
+  if (L == 0) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(0u, 0u);
+    return;
+  }
+  const int c0 = max(0, meta.x), c1 = min(grid - 1, meta.y);
+  if (c1 <= c0) return;  // finished inside one CTA
+  float M = -INFINITY, lsum = 0.f;
+  for (int c = c0 + lane; c <= c1; c += 32) {
+    const float2 ml = p.ws_ml[static_cast<int64_t>(b + c) * p.Hq + hq];
+    const float n = fmaxf(M, ml.x), u = n == -INFINITY ? 0.f : n;
+    lsum = lsum * fast_exp2(M - u) + ml.y * fast_exp2(ml.x - u);
+    M = n;
+  }
+  float top = M;
+#pragma unroll
+  for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  const float u = top == -INFINITY ? 0.f : top;
+  lsum *= fast_exp2(M - u);
+#pragma unroll
+  for (int s = 16; s; s >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, s);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const int64_t row = static_cast<int64_t>(b + c) * p.Hq + hq;
+    const float wgt = fast_exp2(p.ws_ml[row].x - u);
+    const float4 v = *reinterpret_cast<const float4*>(p.ws_o + row * kHeadDim + 4 * lane);
+    acc.x += wgt * v.x;
+    acc.y += wgt * v.y;
+    acc.z += wgt * v.z;
+    acc.w += wgt * v.w;
+  }
+  const float inv = p.v_scale / lsum;
+  *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
+
+// How a call is laid out on the GPU.
+struct Plan {
+  int nt, log2_r, ctas, stages;
+  uint32_t data_bytes, scale_bytes, stage_bytes, q_slot_bytes;
+  size_t smem;
+};
+
+Plan plan_for(int hq, int hkv) {
+  Plan a;
+  const int group = (hq + hkv - 1) / hkv;
+  a.nt = group > 8 ? 2 : 1;
+  const int most = a.nt == 1 ? kMaxHeadWarps : kMaxHeadWarps / 2;
+  // R <= 4: tiles of at most 64 tokens, so that a sequence's last tile wastes little.
+  a.log2_r = 0;
+  while (a.log2_r < 2 && (hkv << (a.log2_r + 1)) <= most) ++a.log2_r;
+  const int warps = hkv << a.log2_r, tile = 16 << a.log2_r;
+  // Few kv heads: several CTAs share an SM (at up to 112 registers a thread).
+  a.ctas = std::max(1, std::min(most / warps, 65536 / (112 * a.nt * 32 * (warps + 1))));
+  a.data_bytes = static_cast<uint32_t>(tile * hkv * q4::kRowBytes);
+  a.scale_bytes = static_cast<uint32_t>(tile * hkv * q4::kRowScales);
+  a.stage_bytes = (2 * (a.data_bytes + a.scale_bytes) + 1023) & ~1023u;
+  a.q_slot_bytes = static_cast<uint32_t>((hq * kHeadDim * 2 + 127) & ~127);
+  const size_t rest = kFixedBytes + kQSlots * a.q_slot_bytes + (a.log2_r ? warps * exchange_bytes(a.nt) : 0);
+  const size_t room = kSmemMax / a.ctas - (a.ctas > 1 ? 1024 : 0);
+  a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (room - rest) / a.stage_bytes));
+  a.smem = rest + static_cast<size_t>(a.stages) * a.stage_bytes;
+  return a;
+}
+
+struct WsLayout {
+  size_t ml, meta, total;
+};
+
+WsLayout ws_layout(int batch, int num_q_heads, int grid) {
+  const size_t slots = static_cast<size_t>(batch) + grid;
+  WsLayout l;
+  l.ml = align256(slots * num_q_heads * kHeadDim * sizeof(float));
+  l.meta = l.ml + align256(slots * num_q_heads * sizeof(float2));
+  l.total = l.meta + align256(static_cast<size_t>(batch) * sizeof(int2));
+  return l;
+}
+
+template <int NT>
+cudaError_t launch(const Plan& pl, const Params& p, const CUtensorMap& km, const CUtensorMap& vm, int grid,
+                   cudaStream_t stream) {
+  static std::atomic<int> smem_set[kMaxDevices];
+  cudaError_t e = ensure_dyn_smem(decode_q4_kernel<NT>, pl.smem, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decode_q4_kernel<NT>, dim3(grid), dim3(32 * ((p.Hkv << p.log2_r) + 1)), pl.smem, stream, km, vm, p);
+}
 
 }  // namespace
 
-// Lane i holds dims 4i .. 4i+3 of the query; keys 0 .. len-1 of the sequence.
-__device__ void attend_row_q4(const Q4Cache& c, const uint16_t* q, uint16_t* out, const int32_t* table, int len,
-                              int kvh, float sl2, unsigned int* err) {
-  const int lane = threadIdx.x & 31;
-  const uint2 w = *reinterpret_cast<const uint2*>(q + 4 * lane);
-  const float x[4] = {q4::bf_lo(w.x), q4::bf_hi(w.x), q4::bf_lo(w.y), q4::bf_hi(w.y)};
-  Acc a;
-  for (int t = 0; t < len; ++t) {
-    int b = __ldg(table + t / kBlockSize);
-    if (b < 0 || b >= c.num_blocks) {
-      if (lane == 0) atomicOr(err, PKV_DEVERR_BLOCK_RANGE);
-      b = 0;
-    }
-    const int64_t row = (static_cast<int64_t>(b) * kBlockSize + t % kBlockSize) * c.num_kv_heads + kvh;
-    uint32_t h[4];
-    q4::dec8(*reinterpret_cast<const uint16_t*>(c.k_data + row * 64 + 2 * lane), h);
-    const float ks = q4::dec_scale(c.k_scales[row * 8 + (lane >> 2)]);
-    float s = ks * (x[0] * q4::half_lo(h[0]) + x[1] * q4::half_hi(h[0]) + x[2] * q4::half_lo(h[1]) +
-                    x[3] * q4::half_hi(h[1]));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= sl2;
-    const float m = fmaxf(a.m, s);
-    const float alpha = fast_exp2(a.m - m), p = fast_exp2(s - m);
-    a.m = m;
-    a.l = a.l * alpha + p;
-    q4::dec8(*reinterpret_cast<const uint16_t*>(c.v_data + row * 64 + 2 * lane), h);
-    const float vs = p * q4::dec_scale(c.v_scales[row * 8 + (lane >> 2)]);
-    a.o[0] = a.o[0] * alpha + vs * q4::half_lo(h[0]);
-    a.o[1] = a.o[1] * alpha + vs * q4::half_hi(h[0]);
-    a.o[2] = a.o[2] * alpha + vs * q4::half_lo(h[1]);
-    a.o[3] = a.o[3] * alpha + vs * q4::half_hi(h[1]);
-  }
-  const float inv = len > 0 ? c.v_scale / a.l : 0.f;
-  *reinterpret_cast<uint2*>(out + 4 * lane) =
-      make_uint2(pack_bf16x2(a.o[0] * inv, a.o[1] * inv), pack_bf16x2(a.o[2] * inv, a.o[3] * inv));
+size_t decode_q4_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_sms) {
+  return ws_layout(batch, num_q_heads, num_sms * plan_for(num_q_heads, num_kv_heads).ctas).total;
 }
 
-__global__ void __launch_bounds__(128) decode_q4_kernel(const AttnQ4Args p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t pair = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (pair >= static_cast<int64_t>(p.num_seqs) * p.num_q_heads) return;
-  const int b = static_cast<int>(pair / p.num_q_heads), h = static_cast<int>(pair % p.num_q_heads);
-  const int lmax = static_cast<int>(min(static_cast<long long>(p.max_seqlen_k),
-                                        static_cast<long long>(p.max_blocks_per_seq) * kBlockSize));
-  int len = p.context_lens[b];
-  if (len < 0 || len > lmax) {
-    if ((threadIdx.x & 31) == 0) atomicOr(&g_err_decode_q4, PKV_DEVERR_LEN_RANGE);
-    len = len < 0 ? 0 : lmax;
-  }
-  attend_row_q4(p.cache, p.q + pair * kHeadDim, p.out + pair * kHeadDim,
-                p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq, len,
-                h / (p.num_q_heads / p.cache.num_kv_heads), p.scale * p.cache.k_scale * 1.4426950408889634f,
-                &g_err_decode_q4);
-}
-
-__global__ void __launch_bounds__(128) prefill_q4_kernel(const AttnQ4Args p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t pair = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int row = static_cast<int>(pair / p.num_q_heads), h = static_cast<int>(pair % p.num_q_heads);
-  const int i = blockIdx.y;
-  const int q0 = p.cu_seqlens_q[i], q1 = p.cu_seqlens_q[i + 1];
-  const int n = q1 - q0, len = p.cu_seqlens_k[i + 1] - p.cu_seqlens_k[i];
-  if (n <= 0) return;
-  if (len < n || len > static_cast<long long>(p.max_blocks_per_seq) * kBlockSize || q1 > p.total_q || q0 < 0 ||
-      n > p.max_seqlen_q || len > p.max_seqlen_k) {
-    if (pair == 0 && threadIdx.x == 0) atomicOr(&g_err_decode_q4, PKV_DEVERR_LEN_RANGE);
-    return;
-  }
-  if (row >= n) return;
-  const int64_t at = (static_cast<int64_t>(q0 + row) * p.num_q_heads + h) * kHeadDim;
-  attend_row_q4(p.cache, p.q + at, p.out + at, p.block_tables + static_cast<int64_t>(i) * p.max_blocks_per_seq,
-                len - n + row + 1, h / (p.num_q_heads / p.cache.num_kv_heads),
-                p.scale * p.cache.k_scale * 1.4426950408889634f, &g_err_decode_q4);
-}
-
-size_t decode_q4_workspace_bytes(int, int, int, int) { return 256; }
-size_t prefill_q4_workspace_bytes(int, int, int, int, int, int, int) { return 256; }
-
-cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int, cudaStream_t stream) {
-  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
-  return launch_pdl(decode_q4_kernel, dim3(static_cast<unsigned>((pairs + 3) / 4)), dim3(128), 0, stream, a);
-}
-
-cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int, cudaStream_t stream) {
-  const int64_t pairs = static_cast<int64_t>(a.max_seqlen_q) * a.num_q_heads;
-  return launch_pdl(prefill_q4_kernel, dim3(static_cast<unsigned>((pairs + 3) / 4), a.num_seqs), dim3(128), 0, stream, a);
+cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
+  const Plan pl = plan_for(a.num_q_heads, a.cache.num_kv_heads);
+  const int grid = num_sms * pl.ctas;
+  const WsLayout wl = ws_layout(a.num_seqs, a.num_q_heads, grid);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  CUtensorMap km, vm;
+  if (!encode_q4_maps(a.cache, 16 << pl.log2_r, a.cache.num_kv_heads, &km, &vm)) return cudaErrorUnknown;
+  Params p = {};
+  p.q = a.q;
+  p.ctx = a.context_lens;
+  p.tables = a.block_tables;
+  p.out = a.out;
+  p.k_scales = a.cache.k_scales;
+  p.v_scales = a.cache.v_scales;
+  p.ws_o = reinterpret_cast<float*>(ws);
+  p.ws_ml = reinterpret_cast<float2*>(ws + wl.ml);
+  p.ws_meta = reinterpret_cast<int2*>(ws + wl.meta);
+  p.maxb = a.max_blocks_per_seq;
+  p.B = a.num_seqs;
+  p.Hq = a.num_q_heads;
+  p.Hkv = a.cache.num_kv_heads;
+  p.G = p.Hq / p.Hkv;
+  p.num_blocks = a.cache.num_blocks;
+  p.lmax = static_cast<int>(std::min<long long>(a.max_seqlen_k, static_cast<long long>(p.maxb) * kBlockSize));
+  p.log2_r = pl.log2_r;
+  p.log2_tile = pl.log2_r + 4;
+  p.tile = 16 << pl.log2_r;
+  p.stages = pl.stages;
+  p.sl2 = a.scale * a.cache.k_scale * 1.4426950408889634f;
+  p.v_scale = a.cache.v_scale;
+  p.data_bytes = pl.data_bytes;
+  p.scale_bytes = pl.scale_bytes;
+  p.stage_bytes = pl.stage_bytes;
+  p.q_slot_bytes = pl.q_slot_bytes;
+  const cudaError_t e = pl.nt == 1 ? launch<1>(pl, p, km, vm, grid, stream) : launch<2>(pl, p, km, vm, grid, stream);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = static_cast<int64_t>(p.B) * p.Hq;
+  return launch_pdl(combine_q4_kernel, dim3(static_cast<unsigned>((pairs + kCombineWarps - 1) / kCombineWarps)),
+                    dim3(32 * kCombineWarps), 0, stream, p, grid);
 }
 
 PKV_DEFINE_READ_ERROR(read_error_decode_q4, g_err_decode_q4)
-cudaError_t read_error_prefill_q4(uint32_t* out, bool) {
-  *out = 0;
-  return cudaSuccess;
-}
 
 }  // namespace pkv
