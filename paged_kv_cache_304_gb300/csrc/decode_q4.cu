@@ -5,15 +5,17 @@
 // codes into matrix operands has to fit into a quarter of the time that the
 // bf16 kernel has.
 //
-// * Work split.  The sequences' tiles of T = 16 R tokens are laid end to end and
+// * Work split.  The sequences' tiles of T = 32 R tokens are laid end to end and
 //   every CTA takes an equal share of the tiles (persistent CTAs, one to three
 //   per SM).  Sequences that straddle CTAs leave partial (max, sum, output)
 //   triples that a combine kernel merges.
 // * Pipeline.  A producer warp fetches a tile's K and V codes for all kv heads
-//   with one TMA tensor copy each ([head][token][64 bytes], 64-byte swizzle) and
-//   the scales, which are contiguous, with plain bulk copies, into a ring.
-// * Operands.  Warp (h, r) computes kv head h for tokens 16r .. 16r+15 of a
-//   tile.  The tokens are the rows of S^T = K Q^T (m16n8k16, fp16 in, fp32
+//   with one TMA tensor copy each and their scales with plain bulk copies into a
+//   ring; a tile is contiguous in memory, so the map sees rows of 128 bytes and
+//   only serves to swizzle them (a map that reordered the tile by head moved 64
+//   bytes a row and held the kernel at 2.5 TB/s).
+// * Operands.  Warp (h, r) computes kv head h for tokens 32r .. 32r+31 of a
+//   tile in two interleaved steps of 16.  The tokens are the rows of S^T = K Q^T (m16n8k16, fp16 in, fp32
 //   out; the group's query heads are the 8 columns) and then the inner dimension
 //   of O^T = V^T P^T, so a group of up to 8 query heads wastes no matrix work on
 //   empty rows.  The order of dims in the first product and of tokens in the
@@ -23,8 +25,8 @@
 //     - for V a lane takes group g of 16 dims of four tokens (8-byte loads, one
 //       scale a token), and exchanges nibbles between two tokens' words, so that
 //       a byte holds the same dim of both: the pair that the operand wants.
-//   Lane g's row of S^T is token tau(g); tau spreads the rows so that both kinds
-//   of load are free of bank conflicts under the 64-byte swizzle.
+//   Lane g's row of S^T is token tau(g); tau pairs odd and even tokens so that
+//   the K loads are free of bank conflicts and the V loads two-way at most.
 //   A byte of two codes becomes two fp16 values in one conversion and one
 //   multiplication by the scale (exact).  The query is scaled by a power of two
 //   per head (its largest element to 2^14 .. 2^15), undone in the softmax scale.
@@ -49,18 +51,17 @@ __device__ unsigned int g_err_decode_q4;
 constexpr int kMaxStages = 6;
 constexpr int kQSlots = 2;      // query staging slots (one per unit in flight)
 constexpr int kMinTokens = 64;  // smallest share of a CTA
-constexpr int kMaxHeadWarps = 16;
+constexpr int kWarpTokens = 32;  // tokens of a tile that one warp handles (two 16-row steps)
+constexpr int kMaxHeadWarps = 8;
 constexpr size_t kSmemMax = 232448;
 
 enum : int32_t { kFirst = 1, kLast = 2, kWhole = 4 };
 
 struct alignas(16) TileHeader {
-  int32_t b;      // sequence, or -1 for "no more work"
+  int32_t b;      // sequence, or -1 for "no more work"; the unit's partial slot is b + CTA index
   int32_t hi;     // the unit ends before token hi
   int32_t t0;     // first token of this tile
   int32_t flags;  // kFirst / kLast tile of the unit; kWhole: unit == sequence
-  int32_t slot;   // partial-result slot of the unit (b + CTA index)
-  int32_t pad[3];
 };
 
 struct Params {
@@ -169,8 +170,6 @@ __device__ void emit_unit(const Params& p, const Smem& sm, const CUtensorMap* km
     h.hi = hi;
     h.t0 = t;
     h.flags = (t == lo ? kFirst : 0) | (t + p.tile >= hi ? kLast : 0) | (lo == 0 && hi == L ? kWhole : 0);
-    h.slot = b + blockIdx.x;
-    h.pad[0] = h.pad[1] = h.pad[2] = 0;
     sm.hdr[st] = h;
     if (h.flags & kFirst) {
       const uint32_t qs = ps.units % kQSlots;
@@ -188,9 +187,10 @@ __device__ void emit_unit(const Params& p, const Smem& sm, const CUtensorMap* km
     mbar_arrive_expect_tx(&sm.full[st], 2 * (p.data_bytes + p.scale_bytes));
     const int tin = t & (kBlockSize - 1);
     const int64_t row = (static_cast<int64_t>(phys) * kBlockSize + tin) * p.Hkv * q4::kRowScales;
-    tma_load_4d(dst, kmap, &sm.full[st], 0, tin, 0, phys);
+    const int row128 = (phys * kBlockSize + tin) / 2 * p.Hkv;  // tin is even; below 2^30 * 8
+    tma_load_2d(dst, kmap, &sm.full[st], 0, row128);
     bulk_g2s(dst + 2 * p.data_bytes, p.k_scales + row, p.scale_bytes, &sm.full[st]);
-    tma_load_4d(dst + p.data_bytes, vmap, &sm.full[st], 0, tin, 0, phys);
+    tma_load_2d(dst + p.data_bytes, vmap, &sm.full[st], 0, row128);
     bulk_g2s(dst + 2 * p.data_bytes + p.scale_bytes, p.v_scales + row, p.scale_bytes, &sm.full[st]);
     ++ps.it;
     if (++ps.stage == static_cast<uint32_t>(p.stages)) {
@@ -287,14 +287,20 @@ __device__ void consumer(const Params& p, const Smem& sm) {
   // tau(2i) = (i & 1) | (i & 2) << 1, tau(2i + 1) = tau(2i) ^ 3, tau(m + 8) = tau(m) + 8
   const int tg = ((((g >> 1) & 1) | ((g >> 2) << 2)) ^ ((g & 1) ? 3 : 0));
   const int ta = (c & 1) | ((c >> 1) << 2), tb = ta ^ 3;
-  const uint32_t head_row = static_cast<uint32_t>(h * p.tile + 16 * r) * q4::kRowBytes;
-  const uint32_t koff = head_row + tg * q4::kRowBytes + ((c ^ ((tg >> 1) & 3)) << 4);
-  const uint32_t va = p.data_bytes + head_row + ta * q4::kRowBytes + (((g >> 1) ^ ((ta >> 1) & 3)) << 4) + (g & 1) * 8;
-  const uint32_t vb = p.data_bytes + head_row + tb * q4::kRowBytes + (((g >> 1) ^ ((tb >> 1) & 3)) << 4) + (g & 1) * 8;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.Hkv) * q4::kRowBytes;
+  // byte `b` of head h's row of token 32r + t of the tile, swizzled
+  auto at = [&](int t, int b) {
+    const uint32_t off = static_cast<uint32_t>(kWarpTokens * r + t) * row_bytes + h * q4::kRowBytes + b;
+    return off ^ (((off >> 7) & 7u) << 4);
+  };
+  const uint32_t ko = at(tg, 16 * c);
+  const uint32_t va = p.data_bytes + at(ta, 8 * g), vb = p.data_bytes + at(tb, 8 * g);
+  // Eight tokens on: 512 Hkv bytes, four swizzle rows for every kv head.
+  const uint32_t step8 = 8 * row_bytes, flip8 = (p.Hkv & 1) * 64u;
   const uint32_t srow = static_cast<uint32_t>(p.Hkv) * q4::kRowScales;  // scale bytes of a token
-  const uint32_t ksoff = 2 * p.data_bytes + (16 * r + tg) * srow + h * q4::kRowScales + 2 * c;
-  const uint32_t vsoff = 2 * p.data_bytes + p.scale_bytes + 16 * r * srow + h * q4::kRowScales + g;
-  const uint32_t vsa = vsoff + ta * srow, vsb = vsoff + tb * srow;
+  const uint32_t sbase = 2 * p.data_bytes + kWarpTokens * r * srow + h * q4::kRowScales;
+  const uint32_t kso = sbase + tg * srow + 2 * c;
+  const uint32_t vsa = sbase + p.scale_bytes + ta * srow + g, vsb = sbase + p.scale_bytes + tb * srow + g;
   const float NEG_INF = -INFINITY;
 
   uint32_t qb[NT][16];   // B operand of the first product: this lane's 32 dims of query head g (+ 8)
@@ -351,57 +357,81 @@ __device__ void consumer(const Params& p, const Smem& sm) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.qempty[qs]);
     }
-    const int t0 = hd.t0 + 16 * r;
-    if (t0 < hd.hi) {
+    const int left = hd.hi - hd.t0 - kWarpTokens * r;  // real tokens of this warp's 32
+    if (left > 0) {
       const uint32_t sb = ring + stage * p.stage_bytes;
-      const uint4 k0 = lds128(sb + koff), k1 = lds128(sb + koff + 8 * q4::kRowBytes);
-      const uint32_t ks0 = lds_u16(sb + ksoff), ks1 = lds_u16(sb + ksoff + 8 * srow);
-      const uint2 v0 = lds64(sb + va), v1 = lds64(sb + vb);
-      const uint2 v2 = lds64(sb + va + 8 * q4::kRowBytes), v3 = lds64(sb + vb + 8 * q4::kRowBytes);
-      uint32_t s0 = lds_u8(sb + vsa), s1 = lds_u8(sb + vsb);
-      uint32_t s2 = lds_u8(sb + vsa + 8 * srow), s3 = lds_u8(sb + vsb + 8 * srow);
+      uint4 kw[4];       // K rows tau(g) + 8i
+      uint32_t ks[4];    // their two scales
+      uint2 vw[8];       // V words of tokens tau(2c), tau(2c + 1), + 8, ...
+      uint32_t vs[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kw[i] = lds128(sb + (ko ^ ((i & 1) * flip8)) + i * step8);
+        ks[i] = lds_u16(sb + kso + i * 8 * srow);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        vw[2 * i] = lds64(sb + (va ^ ((i & 1) * flip8)) + i * step8);
+        vw[2 * i + 1] = lds64(sb + (vb ^ ((i & 1) * flip8)) + i * step8);
+        vs[2 * i] = lds_u8(sb + vsa + i * 8 * srow);
+        vs[2 * i + 1] = lds_u8(sb + vsb + i * 8 * srow);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[stage]);
 
-      // S^T = K Q^T in two chains of four k-steps
-      float sa[NT][4], sc[NT][4];
+      // S^T = K Q^T for the two steps of 16 tokens
+      float s[NT][2][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sa[n][i] = sc[n][i] = 0.f;
-      {
-        const uint32_t f0 = q4::dec_scale2(ks0), f1 = q4::dec_scale2(ks1);
-        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t e0 = i < 2 ? dup_lo(f0) : dup_hi(f0), e1 = i < 2 ? dup_lo(f1) : dup_hi(f1);
+          for (int i = 0; i < 4; ++i) s[n][u][i] = 0.f;
+      uint32_t f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = q4::dec_scale2(ks[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint4 ka = kw[2 * u], kb = kw[2 * u + 1];
+          const uint32_t wa = i == 0 ? ka.x : i == 1 ? ka.y : i == 2 ? ka.z : ka.w;
+          const uint32_t wb = i == 0 ? kb.x : i == 1 ? kb.y : i == 2 ? kb.z : kb.w;
+          const uint32_t ea = i < 2 ? dup_lo(f[2 * u]) : dup_hi(f[2 * u]);
+          const uint32_t eb = i < 2 ? dup_lo(f[2 * u + 1]) : dup_hi(f[2 * u + 1]);
           uint32_t a[4], b[4];
-          q4::dec8(w0[i], a);
-          q4::dec8(w1[i], b);
+          q4::dec8(wa, a);
+          q4::dec8(wb, b);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            a[j] = q4::hmul2(a[j], e0);
-            b[j] = q4::hmul2(b[j], e1);
+            a[j] = q4::hmul2(a[j], ea);
+            b[j] = q4::hmul2(b[j], eb);
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma_f16_16816(sa[n], a[0], b[0], a[1], b[1], qb[n][4 * i], qb[n][4 * i + 1]);
-            mma_f16_16816(sc[n], a[2], b[2], a[3], b[3], qb[n][4 * i + 2], qb[n][4 * i + 3]);
+            mma_f16_16816(s[n][u], a[0], b[0], a[1], b[1], qb[n][4 * i], qb[n][4 * i + 1]);
+            mma_f16_16816(s[n][u], a[2], b[2], a[3], b[3], qb[n][4 * i + 2], qb[n][4 * i + 3]);
           }
         }
       }
-      const int left = hd.hi - t0;  // real tokens of the sixteen
-      const bool ragged = left < 16;
-      uint32_t pb[NT][2];
+      const bool ragged = left < kWarpTokens;
+      uint32_t pb[NT][2][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float x0 = (sa[n][0] + sc[n][0]) * sl[n][0], x1 = (sa[n][1] + sc[n][1]) * sl[n][1];
-        float x2 = (sa[n][2] + sc[n][2]) * sl[n][0], x3 = (sa[n][3] + sc[n][3]) * sl[n][1];
-        if (ragged) {
-          if (tg >= left) x0 = x1 = NEG_INF;
-          if (tg + 8 >= left) x2 = x3 = NEG_INF;
+        float x[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          x[u][0] = s[n][u][0] * sl[n][0];
+          x[u][1] = s[n][u][1] * sl[n][1];
+          x[u][2] = s[n][u][2] * sl[n][0];
+          x[u][3] = s[n][u][3] * sl[n][1];
+          if (ragged) {
+            if (16 * u + tg >= left) x[u][0] = x[u][1] = NEG_INF;
+            if (16 * u + tg + 8 >= left) x[u][2] = x[u][3] = NEG_INF;
+          }
         }
-        const float y0 = fmaxf(x0, x2), y1 = fmaxf(x1, x3);
+        const float y0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+        const float y1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
         if (__any_sync(0xffffffffu, y0 > m[n][0] + 8.f || y1 > m[n][1] + 8.f)) {
           float n0 = y0, n1 = y1;
 #pragma unroll
@@ -427,36 +457,45 @@ __device__ void consumer(const Params& p, const Smem& sm) {
           }
         }
         const float u0 = m[n][0] == NEG_INF ? 0.f : m[n][0], u1 = m[n][1] == NEG_INF ? 0.f : m[n][1];
-        const float p0 = fast_exp2(x0 - u0), p1 = fast_exp2(x1 - u1), p2 = fast_exp2(x2 - u0), p3 = fast_exp2(x3 - u1);
-        l[n][0] += p0 + p2;
-        l[n][1] += p1 + p3;
-        pb[n][0] = movmatrix_trans(pack_f16x2(p0, p1));
-        pb[n][1] = movmatrix_trans(pack_f16x2(p2, p3));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float p0 = fast_exp2(x[u][0] - u0), p1 = fast_exp2(x[u][1] - u1);
+          const float p2 = fast_exp2(x[u][2] - u0), p3 = fast_exp2(x[u][3] - u1);
+          l[n][0] += p0 + p2;
+          l[n][1] += p1 + p3;
+          pb[n][u][0] = movmatrix_trans(pack_f16x2(p0, p1));
+          pb[n][u][1] = movmatrix_trans(pack_f16x2(p2, p3));
+        }
       }
       // O^T += V^T P^T
       if (ragged) {
-        if (ta >= left) s0 = 0;
-        if (tb >= left) s1 = 0;
-        if (ta + 8 >= left) s2 = 0;
-        if (tb + 8 >= left) s3 = 0;
-      }
-      const uint32_t e01 = q4::dec_scale2(s0 | s1 << 8), e23 = q4::dec_scale2(s2 | s3 << 8);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t a0 = half ? v0.y : v0.x, a1 = half ? v1.y : v1.x;
-        const uint32_t a2 = half ? v2.y : v2.x, a3 = half ? v3.y : v3.x;
-        const uint32_t kLow = 0x0f0f0f0fu;
-        uint32_t ev0[4], od0[4], ev1[4], od1[4];
-        q4::dec8((a0 & kLow) | ((a1 << 4) & ~kLow), ev0);
-        q4::dec8(((a0 >> 4) & kLow) | (a1 & ~kLow), od0);
-        q4::dec8((a2 & kLow) | ((a3 << 4) & ~kLow), ev1);
-        q4::dec8(((a2 >> 4) & kLow) | (a3 & ~kLow), od1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t f0 = q4::hmul2(ev0[i], e01), f1 = q4::hmul2(od0[i], e01);
-          const uint32_t f2 = q4::hmul2(ev1[i], e23), f3 = q4::hmul2(od1[i], e23);
+          if (8 * i + ta >= left) vs[2 * i] = 0;
+          if (8 * i + tb >= left) vs[2 * i + 1] = 0;
+        }
+      }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16_16816(acc[n][4 * half + i], f0, f1, f2, f3, pb[n][0], pb[n][1]);
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t e01 = q4::dec_scale2(vs[4 * u] | vs[4 * u + 1] << 8);
+        const uint32_t e23 = q4::dec_scale2(vs[4 * u + 2] | vs[4 * u + 3] << 8);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t a0 = half ? vw[4 * u].y : vw[4 * u].x, a1 = half ? vw[4 * u + 1].y : vw[4 * u + 1].x;
+          const uint32_t a2 = half ? vw[4 * u + 2].y : vw[4 * u + 2].x, a3 = half ? vw[4 * u + 3].y : vw[4 * u + 3].x;
+          const uint32_t kLow = 0x0f0f0f0fu;
+          uint32_t ev0[4], od0[4], ev1[4], od1[4];
+          q4::dec8((a0 & kLow) | ((a1 << 4) & ~kLow), ev0);
+          q4::dec8(((a0 >> 4) & kLow) | (a1 & ~kLow), od0);
+          q4::dec8((a2 & kLow) | ((a3 << 4) & ~kLow), ev1);
+          q4::dec8(((a2 >> 4) & kLow) | (a3 & ~kLow), od1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t f0 = q4::hmul2(ev0[i], e01), f1 = q4::hmul2(od0[i], e01);
+            const uint32_t f2 = q4::hmul2(ev1[i], e23), f3 = q4::hmul2(od1[i], e23);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16_16816(acc[n][4 * half + i], f0, f1, f2, f3, pb[n][u][0], pb[n][u][1]);
+          }
         }
       }
     } else {
@@ -496,7 +535,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float M0 = m[n][0], M1 = m[n][1], L0 = l[n][0], L1 = l[n][1];
-        float w0[4], w1[4];  // weights of the R <= 4 warps
+        float w0[2], w1[2];  // weights of the R <= 2 warps
         if (p.log2_r) {
           M0 = M1 = NEG_INF;
           L0 = L1 = 0.f;
@@ -506,7 +545,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
           }
           const float u0 = M0 == NEG_INF ? 0.f : M0, u1 = M1 == NEG_INF ? 0.f : M1;
 #pragma unroll
-          for (int rr = 0; rr < 4; ++rr) {
+          for (int rr = 0; rr < 2; ++rr) {
             if (rr < R) {
               const float2 e0 = eml[(rr * NT + n) * 8 + 2 * c], e1 = eml[(rr * NT + n) * 8 + 2 * c + 1];
               w0[rr] = fast_exp2(e0.x - u0);
@@ -519,7 +558,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
         const int q0 = 8 * n + 2 * c;  // head of the group
         const bool ok0 = q0 < p.G, ok1 = q0 + 1 < p.G;
         const float inv0 = (hd.flags & kWhole) ? p.v_scale / L0 : 1.f, inv1 = (hd.flags & kWhole) ? p.v_scale / L1 : 1.f;
-        const int64_t row = (static_cast<int64_t>(hd.flags & kWhole ? hd.b : hd.slot) * p.Hq + h * p.G + q0) * kHeadDim + 16 * g;
+        const int64_t row = (static_cast<int64_t>(hd.flags & kWhole ? hd.b : hd.b + static_cast<int>(blockIdx.x)) * p.Hq + h * p.G + q0) * kHeadDim + 16 * g;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (i < i0 || i >= i1) continue;
@@ -527,7 +566,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
           if (p.log2_r) {
             o[0] = o[1] = o[2] = o[3] = 0.f;
 #pragma unroll
-            for (int rr = 0; rr < 4; ++rr) {
+            for (int rr = 0; rr < 2; ++rr) {
               if (rr < R) {
                 const float* e = ex + ((rr * NT + n) * 32 + i * 4) * 32 + lane;
                 o[0] = fmaf(w0[rr], e[0], o[0]);
@@ -546,7 +585,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
           }
         }
         if (!(hd.flags & kWhole) && r == 0 && g == 0) {
-          float2* ml = p.ws_ml + static_cast<int64_t>(hd.slot) * p.Hq + h * p.G + q0;
+          float2* ml = p.ws_ml + static_cast<int64_t>(hd.b + static_cast<int>(blockIdx.x)) * p.Hq + h * p.G + q0;
           if (ok0) ml[0] = make_float2(M0, L0);
           if (ok1) ml[1] = make_float2(M1, L1);
         }
@@ -565,7 +604,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
 }
 
 template <int NT>
-__global__ void __launch_bounds__(NT == 1 ? 32 * (kMaxHeadWarps + 1) : 32 * (kMaxHeadWarps / 2 + 1))
+__global__ void __launch_bounds__(32 * (kMaxHeadWarps + 1), 1)
     decode_q4_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -660,13 +699,11 @@ Plan plan_for(int hq, int hkv) {
   Plan a;
   const int group = (hq + hkv - 1) / hkv;
   a.nt = group > 8 ? 2 : 1;
-  const int most = a.nt == 1 ? kMaxHeadWarps : kMaxHeadWarps / 2;
-  // R <= 4: tiles of at most 64 tokens, so that a sequence's last tile wastes little.
-  a.log2_r = 0;
-  while (a.log2_r < 2 && (hkv << (a.log2_r + 1)) <= most) ++a.log2_r;
-  const int warps = hkv << a.log2_r, tile = 16 << a.log2_r;
-  // Few kv heads: several CTAs share an SM (at up to 112 registers a thread).
-  a.ctas = std::max(1, std::min(most / warps, 65536 / (112 * a.nt * 32 * (warps + 1))));
+  // R <= 2: tiles of at most 64 tokens, so that a sequence's last tile wastes little.
+  a.log2_r = hkv * 2 <= kMaxHeadWarps ? 1 : 0;
+  const int warps = hkv << a.log2_r, tile = kWarpTokens << a.log2_r;
+  // Few kv heads: several CTAs share an SM (at up to 168 registers a thread).
+  a.ctas = std::max(1, std::min(kMaxHeadWarps / warps, 65536 / (168 * 32 * (warps + 1))));
   a.data_bytes = static_cast<uint32_t>(tile * hkv * q4::kRowBytes);
   a.scale_bytes = static_cast<uint32_t>(tile * hkv * q4::kRowScales);
   a.stage_bytes = (2 * (a.data_bytes + a.scale_bytes) + 1023) & ~1023u;
@@ -712,7 +749,7 @@ cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaSt
   const WsLayout wl = ws_layout(a.num_seqs, a.num_q_heads, grid);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   CUtensorMap km, vm;
-  if (!encode_q4_maps(a.cache, 16 << pl.log2_r, a.cache.num_kv_heads, &km, &vm)) return cudaErrorUnknown;
+  if (!encode_q4_maps(a.cache, (kWarpTokens << pl.log2_r) * a.cache.num_kv_heads / 2, &km, &vm)) return cudaErrorUnknown;
   Params p = {};
   p.q = a.q;
   p.ctx = a.context_lens;
@@ -731,8 +768,8 @@ cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaSt
   p.num_blocks = a.cache.num_blocks;
   p.lmax = static_cast<int>(std::min<long long>(a.max_seqlen_k, static_cast<long long>(p.maxb) * kBlockSize));
   p.log2_r = pl.log2_r;
-  p.log2_tile = pl.log2_r + 4;
-  p.tile = 16 << pl.log2_r;
+  p.log2_tile = pl.log2_r + 5;
+  p.tile = kWarpTokens << pl.log2_r;
   p.stages = pl.stages;
   p.sl2 = a.scale * a.cache.k_scale * 1.4426950408889634f;
   p.v_scale = a.cache.v_scale;
