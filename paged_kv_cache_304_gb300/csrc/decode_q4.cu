@@ -48,19 +48,40 @@ namespace {
 
 __device__ unsigned int g_err_decode_q4;
 
-constexpr int kMaxStages = 6;
-constexpr int kQSlots = 2;      // query staging slots (one per unit in flight)
-constexpr int kMinTokens = 64;  // smallest share of a CTA
-constexpr int kWarpTokens = 32;  // tokens of a tile that one warp handles (two 16-row steps)
-constexpr int kMaxHeadWarps = 8;
+constexpr int kMaxStages = 16;
+constexpr int kQSlots = 2;       // query staging slots (one per unit in flight)
+constexpr int kMinTokens = 64;   // smallest share of a CTA
+constexpr int kStepTokens = 32;  // tokens of a ring stage, which one warp per kv head consumes
+constexpr int kMaxLog2R = 3;     // at most 8 warps per kv head
 constexpr size_t kSmemMax = 232448;
+
+// Warps and registers for NT eights of query heads per kv head.  The launch's
+// registers are dealt out again between the consumer warpgroups and the
+// producer's (setmaxnreg); the shares add up to the launch's total.
+template <int NT>
+struct Shape;
+template <>
+struct Shape<1> {
+  static constexpr int kConsumers = 16, kRegsLaunch = 96, kRegsConsumer = 104, kRegsProducer = 64;
+};
+template <>
+struct Shape<2> {
+  static constexpr int kConsumers = 8, kRegsLaunch = 168, kRegsConsumer = 224, kRegsProducer = 56;
+};
+template <int NT>
+constexpr int threads_of() {
+  using S = Shape<NT>;
+  static_assert(S::kConsumers * S::kRegsConsumer + 4 * S::kRegsProducer <= (S::kConsumers + 4) * S::kRegsLaunch,
+                "register shares must fit the launch");
+  return 32 * (S::kConsumers + 4);
+}
 
 enum : int32_t { kFirst = 1, kLast = 2, kWhole = 4 };
 
 struct alignas(16) TileHeader {
   int32_t b;      // sequence, or -1 for "no more work"; the unit's partial slot is b + CTA index
   int32_t hi;     // the unit ends before token hi
-  int32_t t0;     // first token of this tile
+  int32_t t0;     // first token of this stage (it may lie behind hi: nothing to do)
   int32_t flags;  // kFirst / kLast tile of the unit; kWhole: unit == sequence
 };
 
@@ -75,7 +96,7 @@ struct Params {
   float2* ws_ml;  // [slots, Hq] (row max in log2 units, row sum)
   int2* ws_meta;  // [B] first and last CTA holding sequence b
   int32_t maxb, B, Hq, Hkv, G, num_blocks, lmax;
-  int32_t log2_r, tile, log2_tile, stages;  // R, T and the ring's depth
+  int32_t log2_r, log2_tile, stages;  // R, T and the ring's depth
   float sl2;      // scale * k_scale * log2(e)
   float v_scale;
   uint32_t data_bytes, scale_bytes, stage_bytes, q_slot_bytes;
@@ -92,27 +113,24 @@ __device__ __forceinline__ int clamp_len(int L, int lmax) {
 struct Smem {
   uint8_t* stages;
   uint8_t* qbuf;
-  float* ex_o;     // [warp][value][lane]: a warp's output at a unit's end
-  float2* ex_ml;   // [warp][head of the group]
+  float* ex_o;     // [writer][value][lane]: a warp's output at a unit's end
+  float2* ex_ml;   // [writer][head of the group]
   TileHeader* hdr;
   uint64_t *full, *empty, *qfull, *qempty, *xfull, *xempty;
 };
 
-// One warp's exchange area: 32 values per lane and 8 (max, sum) pairs for every
-// eight query heads.
+// Exchange area of a warp that hands its result to the head's first warp: 32
+// values per lane and 8 (max, sum) pairs for every eight query heads.
 __host__ __device__ constexpr uint32_t exchange_bytes(int nt) { return nt * (32 * 32 * 4 + 8 * 8); }
 
 __device__ __forceinline__ Smem carve(uint8_t* base, const Params& p, int nt) {
   Smem s;
-  const int warps = p.Hkv << p.log2_r;
+  const int writers = p.Hkv * ((1 << p.log2_r) - 1);
   s.stages = base;
   s.qbuf = base + p.stages * p.stage_bytes;
   s.ex_o = reinterpret_cast<float*>(s.qbuf + kQSlots * p.q_slot_bytes);
-  uint8_t* after = reinterpret_cast<uint8_t*>(s.ex_o);
-  if (p.log2_r) after += warps * nt * 32 * 32 * 4;
-  s.ex_ml = reinterpret_cast<float2*>(after);
-  if (p.log2_r) after += warps * nt * 64;
-  s.hdr = reinterpret_cast<TileHeader*>(after);
+  s.ex_ml = reinterpret_cast<float2*>(s.ex_o + writers * nt * 32 * 32);
+  s.hdr = reinterpret_cast<TileHeader*>(s.ex_ml + writers * nt * 8);
   s.full = reinterpret_cast<uint64_t*>(s.hdr + kMaxStages);
   s.empty = s.full + kMaxStages;
   s.qfull = s.empty + kMaxStages;
@@ -148,18 +166,14 @@ __device__ __forceinline__ int load_block(const Params& p, int b, int lb) {
   return phys;
 }
 
-// Issue every tile of unit (b, [lo, hi)), lo a multiple of the tile.  Lane 0 of
-// the producer warp only.
+// Issue every tile of unit (b, [lo, hi)), lo a multiple of the tile: R stages of
+// 32 tokens each.  Lane 0 of the producer warp only.
 __device__ void emit_unit(const Params& p, const Smem& sm, const CUtensorMap* kmap, const CUtensorMap* vmap,
                           ProducerState& ps, int b, int lo, int hi, int L, int first_phys) {
   int lb_cur = -1, phys = 0, nxt = first_phys;
-  for (int t = lo; t < hi; t += p.tile) {
-    const int lb = t / kBlockSize;
-    if (lb != lb_cur) {
-      phys = nxt;
-      lb_cur = lb;
-      if ((lb + 1) * kBlockSize < hi) nxt = load_block(p, b, lb + 1);
-    }
+  const int tile = 1 << p.log2_tile;
+  const int end = lo + ((hi - lo + tile - 1) & ~(tile - 1));
+  for (int t = lo; t < end; t += kStepTokens) {
     const uint32_t st = ps.stage;
     if (!mbar_wait(&sm.empty[st], ps.phase ^ 1u, &g_err_decode_q4)) {
       ps.ok = false;
@@ -169,9 +183,9 @@ __device__ void emit_unit(const Params& p, const Smem& sm, const CUtensorMap* km
     h.b = b;
     h.hi = hi;
     h.t0 = t;
-    h.flags = (t == lo ? kFirst : 0) | (t + p.tile >= hi ? kLast : 0) | (lo == 0 && hi == L ? kWhole : 0);
+    h.flags = (t < lo + tile ? kFirst : 0) | (t >= end - tile ? kLast : 0) | (lo == 0 && hi == L ? kWhole : 0);
     sm.hdr[st] = h;
-    if (h.flags & kFirst) {
+    if (t == lo) {
       const uint32_t qs = ps.units % kQSlots;
       if (!mbar_wait(&sm.qempty[qs], ((ps.units / kQSlots) & 1u) ^ 1u, &g_err_decode_q4)) {
         ps.ok = false;
@@ -183,15 +197,24 @@ __device__ void emit_unit(const Params& p, const Smem& sm, const CUtensorMap* km
                &sm.qfull[qs]);
       ++ps.units;
     }
-    uint8_t* dst = sm.stages + st * p.stage_bytes;
-    mbar_arrive_expect_tx(&sm.full[st], 2 * (p.data_bytes + p.scale_bytes));
-    const int tin = t & (kBlockSize - 1);
-    const int64_t row = (static_cast<int64_t>(phys) * kBlockSize + tin) * p.Hkv * q4::kRowScales;
-    const int row128 = (phys * kBlockSize + tin) / 2 * p.Hkv;  // tin is even; below 2^30 * 8
-    tma_load_2d(dst, kmap, &sm.full[st], 0, row128);
-    bulk_g2s(dst + 2 * p.data_bytes, p.k_scales + row, p.scale_bytes, &sm.full[st]);
-    tma_load_2d(dst + p.data_bytes, vmap, &sm.full[st], 0, row128);
-    bulk_g2s(dst + 2 * p.data_bytes + p.scale_bytes, p.v_scales + row, p.scale_bytes, &sm.full[st]);
+    if (t < hi) {
+      const int lb = t / kBlockSize;
+      if (lb != lb_cur) {
+        phys = nxt;
+        lb_cur = lb;
+        if ((lb + 1) * kBlockSize < hi) nxt = load_block(p, b, lb + 1);
+      }
+      uint8_t* dst = sm.stages + st * p.stage_bytes;
+      mbar_arrive_expect_tx(&sm.full[st], 2 * (p.data_bytes + p.scale_bytes));
+      const int slot = phys * kBlockSize + (t & (kBlockSize - 1));
+      const int64_t row = static_cast<int64_t>(slot) * p.Hkv * q4::kRowScales;
+      tma_load_2d(dst, kmap, &sm.full[st], 0, slot / 2 * p.Hkv);  // rows of 128 bytes; below 2^30 * 8
+      bulk_g2s(dst + 2 * p.data_bytes, p.k_scales + row, p.scale_bytes, &sm.full[st]);
+      tma_load_2d(dst + p.data_bytes, vmap, &sm.full[st], 0, slot / 2 * p.Hkv);
+      bulk_g2s(dst + 2 * p.data_bytes + p.scale_bytes, p.v_scales + row, p.scale_bytes, &sm.full[st]);
+    } else {
+      mbar_arrive(&sm.full[st]);
+    }
     ++ps.it;
     if (++ps.stage == static_cast<uint32_t>(p.stages)) {
       ps.stage = 0;
@@ -215,7 +238,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
     prefetch_tensormap(kmap);
     prefetch_tensormap(vmap);
   }
-  const int round = p.tile - 1;
+  const int round = (1 << p.log2_tile) - 1;
   long long total = 0;  // tiles of the batch
   for (int base = 0; base < p.B; base += 32) {
     const int b = base + lane;
@@ -259,10 +282,17 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
       S += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  if (lane == 0 && ps.ok) {
-    if (mbar_wait(&sm.empty[ps.stage], ps.phase ^ 1u, &g_err_decode_q4)) {
+  // One end mark for each of a head's R warps.
+  for (int i = 0; i < 1 << p.log2_r && lane == 0 && ps.ok; ++i) {
+    ps.ok = mbar_wait(&sm.empty[ps.stage], ps.phase ^ 1u, &g_err_decode_q4);
+    if (ps.ok) {
       sm.hdr[ps.stage].b = -1;
       mbar_arrive(&sm.full[ps.stage]);
+      ++ps.it;
+      if (++ps.stage == static_cast<uint32_t>(p.stages)) {
+        ps.stage = 0;
+        ps.phase ^= 1u;
+      }
     }
   }
   if (lane == 0 && !ps.ok) {
@@ -288,9 +318,9 @@ __device__ void consumer(const Params& p, const Smem& sm) {
   const int tg = ((((g >> 1) & 1) | ((g >> 2) << 2)) ^ ((g & 1) ? 3 : 0));
   const int ta = (c & 1) | ((c >> 1) << 2), tb = ta ^ 3;
   const uint32_t row_bytes = static_cast<uint32_t>(p.Hkv) * q4::kRowBytes;
-  // byte `b` of head h's row of token 32r + t of the tile, swizzled
+  // byte `b` of head h's row of the stage's token t, swizzled
   auto at = [&](int t, int b) {
-    const uint32_t off = static_cast<uint32_t>(kWarpTokens * r + t) * row_bytes + h * q4::kRowBytes + b;
+    const uint32_t off = static_cast<uint32_t>(t) * row_bytes + h * q4::kRowBytes + b;
     return off ^ (((off >> 7) & 7u) << 4);
   };
   const uint32_t ko = at(tg, 16 * c);
@@ -298,7 +328,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
   // Eight tokens on: 512 Hkv bytes, four swizzle rows for every kv head.
   const uint32_t step8 = 8 * row_bytes, flip8 = (p.Hkv & 1) * 64u;
   const uint32_t srow = static_cast<uint32_t>(p.Hkv) * q4::kRowScales;  // scale bytes of a token
-  const uint32_t sbase = 2 * p.data_bytes + kWarpTokens * r * srow + h * q4::kRowScales;
+  const uint32_t sbase = 2 * p.data_bytes + h * q4::kRowScales;
   const uint32_t kso = sbase + tg * srow + 2 * c;
   const uint32_t vsa = sbase + p.scale_bytes + ta * srow + g, vsb = sbase + p.scale_bytes + tb * srow + g;
   const float NEG_INF = -INFINITY;
@@ -306,7 +336,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
   uint32_t qb[NT][16];   // B operand of the first product: this lane's 32 dims of query head g (+ 8)
   float acc[NT][8][4];   // O^T: dims 16g + 2i (0, 1) and 16g + 2i + 1 (2, 3) of heads 2c, 2c + 1
   float sl[NT][2], m[NT][2], l[NT][2];
-  uint32_t stage = 0, phase = 0, units = 0;
+  uint32_t stage = r, phase = 0, units = 0;
   const uint32_t ring = smem_u32(sm.stages);
 
   for (;;) {
@@ -357,28 +387,16 @@ __device__ void consumer(const Params& p, const Smem& sm) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.qempty[qs]);
     }
-    const int left = hd.hi - hd.t0 - kWarpTokens * r;  // real tokens of this warp's 32
+    const int left = hd.hi - hd.t0;  // real tokens of the 32
     if (left > 0) {
       const uint32_t sb = ring + stage * p.stage_bytes;
       uint4 kw[4];       // K rows tau(g) + 8i
       uint32_t ks[4];    // their two scales
-      uint2 vw[8];       // V words of tokens tau(2c), tau(2c + 1), + 8, ...
-      uint32_t vs[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         kw[i] = lds128(sb + (ko ^ ((i & 1) * flip8)) + i * step8);
         ks[i] = lds_u16(sb + kso + i * 8 * srow);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        vw[2 * i] = lds64(sb + (va ^ ((i & 1) * flip8)) + i * step8);
-        vw[2 * i + 1] = lds64(sb + (vb ^ ((i & 1) * flip8)) + i * step8);
-        vs[2 * i] = lds_u8(sb + vsa + i * 8 * srow);
-        vs[2 * i + 1] = lds_u8(sb + vsb + i * 8 * srow);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.empty[stage]);
-
       // S^T = K Q^T for the two steps of 16 tokens
       float s[NT][2][4];
 #pragma unroll
@@ -414,7 +432,18 @@ __device__ void consumer(const Params& p, const Smem& sm) {
           }
         }
       }
-      const bool ragged = left < kWarpTokens;
+      uint2 vw[8];       // V words of tokens tau(2c), tau(2c + 1), + 8, ...
+      uint32_t vs[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        vw[2 * i] = lds64(sb + (va ^ ((i & 1) * flip8)) + i * step8);
+        vw[2 * i + 1] = lds64(sb + (vb ^ ((i & 1) * flip8)) + i * step8);
+        vs[2 * i] = lds_u8(sb + vsa + i * 8 * srow);
+        vs[2 * i + 1] = lds_u8(sb + vsb + i * 8 * srow);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[stage]);
+      const bool ragged = left < kStepTokens;
       uint32_t pb[NT][2][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -510,129 +539,121 @@ __device__ void consumer(const Params& p, const Smem& sm) {
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], o);
-      // Merge the R warps of the head through shared memory: each then owns the
-      // dims 16g + 2i of i in [8r / R, 8(r + 1) / R).
-      const int i0 = (8 * r) >> p.log2_r, i1 = (8 * (r + 1)) >> p.log2_r;
-      float* ex = sm.ex_o + static_cast<size_t>(h << p.log2_r) * (NT * 1024);
-      float2* eml = sm.ex_ml + (h << p.log2_r) * (NT * 8);
-      if (p.log2_r) {
+      // The head's other warps hand their results to its first one.
+      float* ex = sm.ex_o + static_cast<size_t>(h * (R - 1)) * (NT * 1024) + lane;
+      float2* eml = sm.ex_ml + h * (R - 1) * (NT * 8) + 2 * c;
+      if (r > 0) {
         if (!mbar_wait(&sm.xempty[h], (units & 1u) ^ 1u, &g_err_decode_q4)) return;
+        ex += (r - 1) * (NT * 1024);
+        eml += (r - 1) * (NT * 8);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) ex[((r * NT + n) * 32 + i * 4 + k) * 32 + lane] = acc[n][i][k];
+            for (int k = 0; k < 4; ++k) ex[(n * 32 + i * 4 + k) * 32] = acc[n][i][k];
           if (g == 0) {
-            eml[(r * NT + n) * 8 + 2 * c] = make_float2(m[n][0], l[n][0]);
-            eml[(r * NT + n) * 8 + 2 * c + 1] = make_float2(m[n][1], l[n][1]);
+            eml[n * 8] = make_float2(m[n][0], l[n][0]);
+            eml[n * 8 + 1] = make_float2(m[n][1], l[n][1]);
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.xfull[h]);
-        if (!mbar_wait(&sm.xfull[h], units & 1u, &g_err_decode_q4)) return;
-      }
+      } else {
+        if (R > 1) {
+          if (!mbar_wait(&sm.xfull[h], units & 1u, &g_err_decode_q4)) return;
+          for (int rr = 1; rr < R; ++rr, ex += NT * 1024, eml += NT * 8) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float M0 = m[n][0], M1 = m[n][1], L0 = l[n][0], L1 = l[n][1];
-        float w0[2], w1[2];  // weights of the R <= 2 warps
-        if (p.log2_r) {
-          M0 = M1 = NEG_INF;
-          L0 = L1 = 0.f;
-          for (int rr = 0; rr < R; ++rr) {
-            M0 = fmaxf(M0, eml[(rr * NT + n) * 8 + 2 * c].x);
-            M1 = fmaxf(M1, eml[(rr * NT + n) * 8 + 2 * c + 1].x);
-          }
-          const float u0 = M0 == NEG_INF ? 0.f : M0, u1 = M1 == NEG_INF ? 0.f : M1;
+            for (int n = 0; n < NT; ++n) {
+              const float2 e0 = eml[n * 8], e1 = eml[n * 8 + 1];
+              const float M0 = fmaxf(m[n][0], e0.x), M1 = fmaxf(m[n][1], e1.x);
+              const float u0 = M0 == NEG_INF ? 0.f : M0, u1 = M1 == NEG_INF ? 0.f : M1;
+              const float a0 = fast_exp2(m[n][0] - u0), a1 = fast_exp2(m[n][1] - u1);
+              const float b0 = fast_exp2(e0.x - u0), b1 = fast_exp2(e1.x - u1);
+              m[n][0] = M0;
+              m[n][1] = M1;
+              l[n][0] = l[n][0] * a0 + e0.y * b0;
+              l[n][1] = l[n][1] * a1 + e1.y * b1;
 #pragma unroll
-          for (int rr = 0; rr < 2; ++rr) {
-            if (rr < R) {
-              const float2 e0 = eml[(rr * NT + n) * 8 + 2 * c], e1 = eml[(rr * NT + n) * 8 + 2 * c + 1];
-              w0[rr] = fast_exp2(e0.x - u0);
-              w1[rr] = fast_exp2(e1.x - u1);
-              L0 += w0[rr] * e0.y;
-              L1 += w1[rr] * e1.y;
+              for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  acc[n][i][k] = acc[n][i][k] * (k & 1 ? a1 : a0) + ex[(n * 32 + i * 4 + k) * 32] * (k & 1 ? b1 : b0);
             }
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.xempty[h]);
         }
-        const int q0 = 8 * n + 2 * c;  // head of the group
-        const bool ok0 = q0 < p.G, ok1 = q0 + 1 < p.G;
-        const float inv0 = (hd.flags & kWhole) ? p.v_scale / L0 : 1.f, inv1 = (hd.flags & kWhole) ? p.v_scale / L1 : 1.f;
-        const int64_t row = (static_cast<int64_t>(hd.flags & kWhole ? hd.b : hd.b + static_cast<int>(blockIdx.x)) * p.Hq + h * p.G + q0) * kHeadDim + 16 * g;
+        const bool whole = hd.flags & kWhole;
+        const int64_t row = whole ? hd.b : hd.b + static_cast<int>(blockIdx.x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i < i0 || i >= i1) continue;
-          float o[4] = {acc[n][i][0], acc[n][i][1], acc[n][i][2], acc[n][i][3]};
-          if (p.log2_r) {
-            o[0] = o[1] = o[2] = o[3] = 0.f;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int rr = 0; rr < 2; ++rr) {
-              if (rr < R) {
-                const float* e = ex + ((rr * NT + n) * 32 + i * 4) * 32 + lane;
-                o[0] = fmaf(w0[rr], e[0], o[0]);
-                o[1] = fmaf(w1[rr], e[32], o[1]);
-                o[2] = fmaf(w0[rr], e[64], o[2]);
-                o[3] = fmaf(w1[rr], e[96], o[3]);
-              }
+          for (int k = 0; k < 2; ++k) {
+            const int head = 8 * n + 2 * c + k;
+            if (head >= p.G) continue;
+            const int64_t at = row * p.Hq + h * p.G + head;
+            if (whole) {
+              const float inv = p.v_scale / l[n][k];
+              uint32_t o[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(acc[n][i][k] * inv, acc[n][i][k + 2] * inv);
+              uint4* dst = reinterpret_cast<uint4*>(p.out + at * kHeadDim + 16 * g);
+              dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+              dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.ws_o + at * kHeadDim + 16 * g);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_float4(acc[n][2 * i][k], acc[n][2 * i][k + 2], acc[n][2 * i + 1][k], acc[n][2 * i + 1][k + 2]);
+              if (g == 0) p.ws_ml[at] = make_float2(m[n][k], l[n][k]);
             }
           }
-          if (hd.flags & kWhole) {
-            if (ok0) *reinterpret_cast<uint32_t*>(p.out + row + 2 * i) = pack_bf16x2(o[0] * inv0, o[2] * inv0);
-            if (ok1) *reinterpret_cast<uint32_t*>(p.out + row + kHeadDim + 2 * i) = pack_bf16x2(o[1] * inv1, o[3] * inv1);
-          } else {
-            if (ok0) *reinterpret_cast<float2*>(p.ws_o + row + 2 * i) = make_float2(o[0], o[2]);
-            if (ok1) *reinterpret_cast<float2*>(p.ws_o + row + kHeadDim + 2 * i) = make_float2(o[1], o[3]);
-          }
-        }
-        if (!(hd.flags & kWhole) && r == 0 && g == 0) {
-          float2* ml = p.ws_ml + static_cast<int64_t>(hd.b + static_cast<int>(blockIdx.x)) * p.Hq + h * p.G + q0;
-          if (ok0) ml[0] = make_float2(M0, L0);
-          if (ok1) ml[1] = make_float2(M1, L1);
-        }
-      }
-      if (p.log2_r) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.xempty[h]);
       }
       ++units;
     }
-    if (++stage == static_cast<uint32_t>(p.stages)) {
-      stage = 0;
+    stage += R;
+    if (stage >= static_cast<uint32_t>(p.stages)) {
+      stage -= p.stages;
       phase ^= 1u;
     }
   }
 }
 
 template <int NT>
-__global__ void __launch_bounds__(32 * (kMaxHeadWarps + 1), 1)
+__global__ void __launch_bounds__(threads_of<NT>(), 1)
     decode_q4_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
   const Smem sm = carve(base, p, NT);
-  const int warp = threadIdx.x >> 5, warps = p.Hkv << p.log2_r;
+  const int warp = threadIdx.x >> 5, R = 1 << p.log2_r;
   griddep_wait();
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], warps);
+      mbar_init(&sm.empty[s], p.Hkv);
     }
     for (int s = 0; s < kQSlots; ++s) {
       mbar_init(&sm.qfull[s], 1);
-      mbar_init(&sm.qempty[s], warps);
+      mbar_init(&sm.qempty[s], p.Hkv << p.log2_r);
     }
     for (int s = 0; s < p.Hkv; ++s) {
-      mbar_init(&sm.xfull[s], 1 << p.log2_r);
-      mbar_init(&sm.xempty[s], 1 << p.log2_r);
+      mbar_init(&sm.xfull[s], max(1, R - 1));
+      mbar_init(&sm.xempty[s], 1);
     }
     fence_barrier_init();
   }
   __syncthreads();
-  if (warp == warps)
-    producer(p, sm, &kmap, &vmap);
-  else
-    consumer<NT>(p, sm);
+  using S = Shape<NT>;
+  if (warp >= S::kConsumers) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsProducer));
+    if (warp == S::kConsumers) producer(p, sm, &kmap, &vmap);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsConsumer));
+    if (warp < (p.Hkv << p.log2_r)) consumer<NT>(p, sm);
+  }
 }
 
 // Merge the partials of sequences that straddle CTAs; zero pad rows.  One warp
@@ -690,27 +711,23 @@ size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
 
 // How a call is laid out on the GPU.
 struct Plan {
-  int nt, log2_r, ctas, stages;
+  int nt, log2_r, stages;
   uint32_t data_bytes, scale_bytes, stage_bytes, q_slot_bytes;
   size_t smem;
 };
 
 Plan plan_for(int hq, int hkv) {
   Plan a;
-  const int group = (hq + hkv - 1) / hkv;
-  a.nt = group > 8 ? 2 : 1;
-  // R <= 2: tiles of at most 64 tokens, so that a sequence's last tile wastes little.
-  a.log2_r = hkv * 2 <= kMaxHeadWarps ? 1 : 0;
-  const int warps = hkv << a.log2_r, tile = kWarpTokens << a.log2_r;
-  // Few kv heads: several CTAs share an SM (at up to 168 registers a thread).
-  a.ctas = std::max(1, std::min(kMaxHeadWarps / warps, 65536 / (168 * 32 * (warps + 1))));
-  a.data_bytes = static_cast<uint32_t>(tile * hkv * q4::kRowBytes);
-  a.scale_bytes = static_cast<uint32_t>(tile * hkv * q4::kRowScales);
+  a.nt = hq > 8 * hkv ? 2 : 1;
+  const int most = a.nt == 1 ? Shape<1>::kConsumers : Shape<2>::kConsumers;
+  a.log2_r = 0;
+  while (a.log2_r < kMaxLog2R && (hkv << (a.log2_r + 1)) <= most) ++a.log2_r;
+  a.data_bytes = static_cast<uint32_t>(kStepTokens * hkv * q4::kRowBytes);
+  a.scale_bytes = static_cast<uint32_t>(kStepTokens * hkv * q4::kRowScales);
   a.stage_bytes = (2 * (a.data_bytes + a.scale_bytes) + 1023) & ~1023u;
-  a.q_slot_bytes = static_cast<uint32_t>((hq * kHeadDim * 2 + 127) & ~127);
-  const size_t rest = kFixedBytes + kQSlots * a.q_slot_bytes + (a.log2_r ? warps * exchange_bytes(a.nt) : 0);
-  const size_t room = kSmemMax / a.ctas - (a.ctas > 1 ? 1024 : 0);
-  a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (room - rest) / a.stage_bytes));
+  a.q_slot_bytes = static_cast<uint32_t>(hq * kHeadDim * 2);
+  const size_t rest = kFixedBytes + kQSlots * a.q_slot_bytes + hkv * ((1 << a.log2_r) - 1) * exchange_bytes(a.nt);
+  a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemMax - rest) / a.stage_bytes));
   a.smem = rest + static_cast<size_t>(a.stages) * a.stage_bytes;
   return a;
 }
@@ -731,25 +748,35 @@ WsLayout ws_layout(int batch, int num_q_heads, int grid) {
 template <int NT>
 cudaError_t launch(const Plan& pl, const Params& p, const CUtensorMap& km, const CUtensorMap& vm, int grid,
                    cudaStream_t stream) {
+  // The warpgroups' requests for registers can only be met if the kernel was
+  // built with exactly the launch's share per thread.
+  static std::atomic<int> regs_checked{0};
+  if (!regs_checked.load(std::memory_order_acquire)) {
+    cudaFuncAttributes fa{};
+    const cudaError_t e = cudaFuncGetAttributes(&fa, decode_q4_kernel<NT>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != Shape<NT>::kRegsLaunch) return cudaErrorInvalidKernelImage;
+    regs_checked.store(1, std::memory_order_release);
+  }
   static std::atomic<int> smem_set[kMaxDevices];
-  cudaError_t e = ensure_dyn_smem(decode_q4_kernel<NT>, pl.smem, smem_set);
+  const cudaError_t e = ensure_dyn_smem(decode_q4_kernel<NT>, pl.smem, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_q4_kernel<NT>, dim3(grid), dim3(32 * ((p.Hkv << p.log2_r) + 1)), pl.smem, stream, km, vm, p);
+  return launch_pdl(decode_q4_kernel<NT>, dim3(grid), dim3(threads_of<NT>()), pl.smem, stream, km, vm, p);
 }
 
 }  // namespace
 
-size_t decode_q4_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_sms) {
-  return ws_layout(batch, num_q_heads, num_sms * plan_for(num_q_heads, num_kv_heads).ctas).total;
+size_t decode_q4_workspace_bytes(int batch, int num_q_heads, int, int num_sms) {
+  return ws_layout(batch, num_q_heads, num_sms).total;
 }
 
 cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
   const Plan pl = plan_for(a.num_q_heads, a.cache.num_kv_heads);
-  const int grid = num_sms * pl.ctas;
+  const int grid = num_sms;
   const WsLayout wl = ws_layout(a.num_seqs, a.num_q_heads, grid);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   CUtensorMap km, vm;
-  if (!encode_q4_maps(a.cache, (kWarpTokens << pl.log2_r) * a.cache.num_kv_heads / 2, &km, &vm)) return cudaErrorUnknown;
+  if (!encode_q4_maps(a.cache, kStepTokens * a.cache.num_kv_heads / 2, &km, &vm)) return cudaErrorUnknown;
   Params p = {};
   p.q = a.q;
   p.ctx = a.context_lens;
@@ -768,8 +795,7 @@ cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaSt
   p.num_blocks = a.cache.num_blocks;
   p.lmax = static_cast<int>(std::min<long long>(a.max_seqlen_k, static_cast<long long>(p.maxb) * kBlockSize));
   p.log2_r = pl.log2_r;
-  p.log2_tile = pl.log2_r + 5;
-  p.tile = kWarpTokens << pl.log2_r;
+  p.log2_tile = pl.log2_r + 5;  // tiles of 32 R tokens
   p.stages = pl.stages;
   p.sl2 = a.scale * a.cache.k_scale * 1.4426950408889634f;
   p.v_scale = a.cache.v_scale;
