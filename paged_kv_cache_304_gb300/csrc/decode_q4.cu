@@ -10,10 +10,9 @@
 //   per SM).  Sequences that straddle CTAs leave partial (max, sum, output)
 //   triples that a combine kernel merges.
 // * Pipeline.  A producer warp fetches a tile's K and V codes for all kv heads
-//   with one TMA tensor copy each and their scales with plain bulk copies into a
-//   ring; a tile is contiguous in memory, so the map sees rows of 128 bytes and
-//   only serves to swizzle them (a map that reordered the tile by head moved 64
-//   bytes a row and held the kernel at 2.5 TB/s).
+//   with one TMA tensor copy each, laid out [head][token][64 bytes] with the
+//   64-byte swizzle, and the scales, which are contiguous, with plain bulk copies
+//   into a ring of 32-token stages.
 // * Operands.  Warp (h, r) computes kv head h for tokens 32r .. 32r+31 of a
 //   tile in two interleaved steps of 16.  The tokens are the rows of S^T = K Q^T (m16n8k16, fp16 in, fp32
 //   out; the group's query heads are the 8 columns) and then the inner dimension
@@ -26,7 +25,7 @@
 //       scale a token), and exchanges nibbles between two tokens' words, so that
 //       a byte holds the same dim of both: the pair that the operand wants.
 //   Lane g's row of S^T is token tau(g); tau pairs odd and even tokens so that
-//   the K loads are free of bank conflicts and the V loads two-way at most.
+//   both kinds of load are free of bank conflicts under the swizzle.
 //   A byte of two codes becomes two fp16 values in one conversion and one
 //   multiplication by the scale (exact).  The query is scaled by a power of two
 //   per head (its largest element to 2^14 .. 2^15), undone in the softmax scale.
@@ -38,6 +37,8 @@
 // * Waits are bounded: a wait that exceeds two seconds sets
 //   PKV_DEVERR_WAIT_TIMEOUT and the CTA returns.
 #include <cuda_runtime.h>
+
+#include <cfloat>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -206,11 +207,11 @@ __device__ void emit_unit(const Params& p, const Smem& sm, const CUtensorMap* km
       }
       uint8_t* dst = sm.stages + st * p.stage_bytes;
       mbar_arrive_expect_tx(&sm.full[st], 2 * (p.data_bytes + p.scale_bytes));
-      const int slot = phys * kBlockSize + (t & (kBlockSize - 1));
-      const int64_t row = static_cast<int64_t>(slot) * p.Hkv * q4::kRowScales;
-      tma_load_2d(dst, kmap, &sm.full[st], 0, slot / 2 * p.Hkv);  // rows of 128 bytes; below 2^30 * 8
+      const int tin = t & (kBlockSize - 1);
+      const int64_t row = (static_cast<int64_t>(phys) * kBlockSize + tin) * p.Hkv * q4::kRowScales;
+      tma_load_4d(dst, kmap, &sm.full[st], 0, tin, 0, phys);
       bulk_g2s(dst + 2 * p.data_bytes, p.k_scales + row, p.scale_bytes, &sm.full[st]);
-      tma_load_2d(dst + p.data_bytes, vmap, &sm.full[st], 0, slot / 2 * p.Hkv);
+      tma_load_4d(dst + p.data_bytes, vmap, &sm.full[st], 0, tin, 0, phys);
       bulk_g2s(dst + 2 * p.data_bytes + p.scale_bytes, p.v_scales + row, p.scale_bytes, &sm.full[st]);
     } else {
       mbar_arrive(&sm.full[st]);
@@ -238,12 +239,23 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
     prefetch_tensormap(kmap);
     prefetch_tensormap(vmap);
   }
+  // Lengths are loaded 256 at a time, all loads together; a batch of at most
+  // 256 sequences is loaded once for both passes.
   const int round = (1 << p.log2_tile) - 1;
+  int len[8];
+  auto load_lengths = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) len[i] = base + 32 * i + lane < p.B ? __ldg(p.ctx + base + 32 * i + lane) : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) len[i] = clamp_len(len[i], p.lmax);
+  };
   long long total = 0;  // tiles of the batch
-  for (int base = 0; base < p.B; base += 32) {
-    const int b = base + lane;
-    const int L = b < p.B ? clamp_len(__ldg(p.ctx + b), p.lmax) : 0;
-    total += __reduce_add_sync(0xffffffffu, static_cast<unsigned>((L + round) >> p.log2_tile));
+  for (int base = 0; base < p.B; base += 256) {
+    load_lengths(base);
+    unsigned n = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n += static_cast<unsigned>((len[i] + round) >> p.log2_tile);
+    total += __reduce_add_sync(0xffffffffu, n);
   }
   ProducerState ps;
   if (total > 0) {
@@ -254,8 +266,11 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
     const long long my_hi = my_lo + per < total ? my_lo + per : total;
     long long S = 0;
     for (int base = 0; base < p.B && S < my_hi && ps.ok; base += 32) {
+      if ((base & 255) == 0 && p.B > 256) load_lengths(base);
       const int b = base + lane;
-      const int L = b < p.B ? clamp_len(__ldg(p.ctx + b), p.lmax) : 0;
+      int L = len[0];
+#pragma unroll
+      for (int i = 0; i < 7; ++i) len[i] = len[i + 1];
       const int n = (L + round) >> p.log2_tile;
       const int incl = warp_incl_scan(n, lane);
       const long long Sb = S + incl - n;
@@ -317,21 +332,17 @@ __device__ void consumer(const Params& p, const Smem& sm) {
   // tau(2i) = (i & 1) | (i & 2) << 1, tau(2i + 1) = tau(2i) ^ 3, tau(m + 8) = tau(m) + 8
   const int tg = ((((g >> 1) & 1) | ((g >> 2) << 2)) ^ ((g & 1) ? 3 : 0));
   const int ta = (c & 1) | ((c >> 1) << 2), tb = ta ^ 3;
-  const uint32_t row_bytes = static_cast<uint32_t>(p.Hkv) * q4::kRowBytes;
-  // byte `b` of head h's row of the stage's token t, swizzled
-  auto at = [&](int t, int b) {
-    const uint32_t off = static_cast<uint32_t>(t) * row_bytes + h * q4::kRowBytes + b;
-    return off ^ (((off >> 7) & 7u) << 4);
+  // 16-byte chunk of head h's row of token t (swizzled; 8 tokens on is 512 bytes on)
+  auto at = [&](int t, int chunk) {
+    return static_cast<uint32_t>((h * kStepTokens + t) * q4::kRowBytes + ((chunk ^ ((t >> 1) & 3)) << 4));
   };
-  const uint32_t ko = at(tg, 16 * c);
-  const uint32_t va = p.data_bytes + at(ta, 8 * g), vb = p.data_bytes + at(tb, 8 * g);
-  // Eight tokens on: 512 Hkv bytes, four swizzle rows for every kv head.
-  const uint32_t step8 = 8 * row_bytes, flip8 = (p.Hkv & 1) * 64u;
+  const uint32_t ko = at(tg, c);
+  const uint32_t va = p.data_bytes + at(ta, g >> 1) + (g & 1) * 8, vb = p.data_bytes + at(tb, g >> 1) + (g & 1) * 8;
   const uint32_t srow = static_cast<uint32_t>(p.Hkv) * q4::kRowScales;  // scale bytes of a token
   const uint32_t sbase = 2 * p.data_bytes + h * q4::kRowScales;
   const uint32_t kso = sbase + tg * srow + 2 * c;
   const uint32_t vsa = sbase + p.scale_bytes + ta * srow + g, vsb = sbase + p.scale_bytes + tb * srow + g;
-  const float NEG_INF = -INFINITY;
+  const float kLowest = -FLT_MAX;  // maximum of no scores: factors 2^(kLowest - m) are zero
 
   uint32_t qb[NT][16];   // B operand of the first product: this lane's 32 dims of query head g (+ 8)
   float acc[NT][8][4];   // O^T: dims 16g + 2i (0, 1) and 16g + 2i + 1 (2, 3) of heads 2c, 2c + 1
@@ -379,7 +390,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
         for (int j = 0; j < 16; ++j) qb[n][j] = pack_f16x2(x[2 * j] * f, x[2 * j + 1] * f);
         sl[n][0] = p.sl2 * __shfl_sync(0xffffffffu, inv, 8 * c);
         sl[n][1] = p.sl2 * __shfl_sync(0xffffffffu, inv, 8 * c + 4);
-        m[n][0] = m[n][1] = NEG_INF;
+        m[n][0] = m[n][1] = kLowest;
         l[n][0] = l[n][1] = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
@@ -394,7 +405,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
       uint32_t ks[4];    // their two scales
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        kw[i] = lds128(sb + (ko ^ ((i & 1) * flip8)) + i * step8);
+        kw[i] = lds128(sb + ko + i * 512);
         ks[i] = lds_u16(sb + kso + i * 8 * srow);
       }
       // S^T = K Q^T for the two steps of 16 tokens
@@ -436,8 +447,8 @@ __device__ void consumer(const Params& p, const Smem& sm) {
       uint32_t vs[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        vw[2 * i] = lds64(sb + (va ^ ((i & 1) * flip8)) + i * step8);
-        vw[2 * i + 1] = lds64(sb + (vb ^ ((i & 1) * flip8)) + i * step8);
+        vw[2 * i] = lds64(sb + va + i * 512);
+        vw[2 * i + 1] = lds64(sb + vb + i * 512);
         vs[2 * i] = lds_u8(sb + vsa + i * 8 * srow);
         vs[2 * i + 1] = lds_u8(sb + vsb + i * 8 * srow);
       }
@@ -447,20 +458,15 @@ __device__ void consumer(const Params& p, const Smem& sm) {
       uint32_t pb[NT][2][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float x[2][4];
+        if (ragged) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          x[u][0] = s[n][u][0] * sl[n][0];
-          x[u][1] = s[n][u][1] * sl[n][1];
-          x[u][2] = s[n][u][2] * sl[n][0];
-          x[u][3] = s[n][u][3] * sl[n][1];
-          if (ragged) {
-            if (16 * u + tg >= left) x[u][0] = x[u][1] = NEG_INF;
-            if (16 * u + tg + 8 >= left) x[u][2] = x[u][3] = NEG_INF;
+          for (int u = 0; u < 2; ++u) {
+            if (16 * u + tg >= left) s[n][u][0] = s[n][u][1] = -INFINITY;
+            if (16 * u + tg + 8 >= left) s[n][u][2] = s[n][u][3] = -INFINITY;
           }
         }
-        const float y0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-        const float y1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+        const float y0 = fmaxf(fmax3(s[n][0][0], s[n][0][2], s[n][1][0]), s[n][1][2]) * sl[n][0];
+        const float y1 = fmaxf(fmax3(s[n][0][1], s[n][0][3], s[n][1][1]), s[n][1][3]) * sl[n][1];
         if (__any_sync(0xffffffffu, y0 > m[n][0] + 8.f || y1 > m[n][1] + 8.f)) {
           float n0 = y0, n1 = y1;
 #pragma unroll
@@ -470,9 +476,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
           }
           n0 = fmaxf(n0, m[n][0]);
           n1 = fmaxf(n1, m[n][1]);
-          // a head of the group beyond its size, or none seen yet: -inf stays, factor 1
-          const float a0 = n0 == NEG_INF ? 1.f : fast_exp2(m[n][0] - n0);
-          const float a1 = n1 == NEG_INF ? 1.f : fast_exp2(m[n][1] - n1);
+          const float a0 = fast_exp2(m[n][0] - n0), a1 = fast_exp2(m[n][1] - n1);
           m[n][0] = n0;
           m[n][1] = n1;
           l[n][0] *= a0;
@@ -485,11 +489,12 @@ __device__ void consumer(const Params& p, const Smem& sm) {
             acc[n][i][3] *= a1;
           }
         }
-        const float u0 = m[n][0] == NEG_INF ? 0.f : m[n][0], u1 = m[n][1] == NEG_INF ? 0.f : m[n][1];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float p0 = fast_exp2(x[u][0] - u0), p1 = fast_exp2(x[u][1] - u1);
-          const float p2 = fast_exp2(x[u][2] - u0), p3 = fast_exp2(x[u][3] - u1);
+          const float p0 = fast_exp2(fmaf(s[n][u][0], sl[n][0], -m[n][0]));
+          const float p1 = fast_exp2(fmaf(s[n][u][1], sl[n][1], -m[n][1]));
+          const float p2 = fast_exp2(fmaf(s[n][u][2], sl[n][0], -m[n][0]));
+          const float p3 = fast_exp2(fmaf(s[n][u][3], sl[n][1], -m[n][1]));
           l[n][0] += p0 + p2;
           l[n][1] += p1 + p3;
           pb[n][u][0] = movmatrix_trans(pack_f16x2(p0, p1));
@@ -567,9 +572,8 @@ __device__ void consumer(const Params& p, const Smem& sm) {
             for (int n = 0; n < NT; ++n) {
               const float2 e0 = eml[n * 8], e1 = eml[n * 8 + 1];
               const float M0 = fmaxf(m[n][0], e0.x), M1 = fmaxf(m[n][1], e1.x);
-              const float u0 = M0 == NEG_INF ? 0.f : M0, u1 = M1 == NEG_INF ? 0.f : M1;
-              const float a0 = fast_exp2(m[n][0] - u0), a1 = fast_exp2(m[n][1] - u1);
-              const float b0 = fast_exp2(e0.x - u0), b1 = fast_exp2(e1.x - u1);
+              const float a0 = fast_exp2(m[n][0] - M0), a1 = fast_exp2(m[n][1] - M1);
+              const float b0 = fast_exp2(e0.x - M0), b1 = fast_exp2(e1.x - M1);
               m[n][0] = M0;
               m[n][1] = M1;
               l[n][0] = l[n][0] * a0 + e0.y * b0;
@@ -678,25 +682,24 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_q4_kernel(const Pa
   }
   const int c0 = max(0, meta.x), c1 = min(grid - 1, meta.y);
   if (c1 <= c0) return;  // finished inside one CTA
-  float M = -INFINITY, lsum = 0.f;
+  float M = -FLT_MAX, lsum = 0.f;
   for (int c = c0 + lane; c <= c1; c += 32) {
     const float2 ml = p.ws_ml[static_cast<int64_t>(b + c) * p.Hq + hq];
-    const float n = fmaxf(M, ml.x), u = n == -INFINITY ? 0.f : n;
-    lsum = lsum * fast_exp2(M - u) + ml.y * fast_exp2(ml.x - u);
+    const float n = fmaxf(M, ml.x);
+    lsum = lsum * fast_exp2(M - n) + ml.y * fast_exp2(ml.x - n);
     M = n;
   }
   float top = M;
 #pragma unroll
   for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  const float u = top == -INFINITY ? 0.f : top;
-  lsum *= fast_exp2(M - u);
+  lsum *= fast_exp2(M - top);
 #pragma unroll
   for (int s = 16; s; s >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, s);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int c = c0; c <= c1; ++c) {
     const int64_t row = static_cast<int64_t>(b + c) * p.Hq + hq;
-    const float wgt = fast_exp2(p.ws_ml[row].x - u);
+    const float wgt = fast_exp2(p.ws_ml[row].x - top);
     const float4 v = *reinterpret_cast<const float4*>(p.ws_o + row * kHeadDim + 4 * lane);
     acc.x += wgt * v.x;
     acc.y += wgt * v.y;
@@ -776,7 +779,7 @@ cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaSt
   const WsLayout wl = ws_layout(a.num_seqs, a.num_q_heads, grid);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   CUtensorMap km, vm;
-  if (!encode_q4_maps(a.cache, kStepTokens * a.cache.num_kv_heads / 2, &km, &vm)) return cudaErrorUnknown;
+  if (!encode_q4_maps(a.cache, kStepTokens, a.cache.num_kv_heads, &km, &vm)) return cudaErrorUnknown;
   Params p = {};
   p.q = a.q;
   p.ctx = a.context_lens;

@@ -87,17 +87,17 @@ bool encode_cache_maps(const void* k_cache, const void* v_cache, int num_blocks,
 
 }  // namespace
 
-bool encode_q4_maps(const Q4Cache& c, int rows, CUtensorMap* k, CUtensorMap* v) {
+bool encode_q4_maps(const Q4Cache& c, int tokens, int heads, CUtensorMap* k, CUtensorMap* v) {
   auto enc = encode_fn();
   if (!enc) return false;
-  // A block's codes are 256 * Hkv * 64 bytes, a multiple of 128.
-  cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(c.num_blocks) * (kBlockSize * 64 / 128) * c.num_kv_heads};
-  cuuint64_t strides[1] = {128};
-  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(rows)};
-  cuuint32_t es[2] = {1, 1};
+  const cuuint64_t row = static_cast<cuuint64_t>(c.num_kv_heads) * 64;
+  cuuint64_t dims[4] = {64, kBlockSize, static_cast<cuuint64_t>(c.num_kv_heads), static_cast<cuuint64_t>(c.num_blocks)};
+  cuuint64_t strides[3] = {row, 64, row * kBlockSize};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(tokens), static_cast<cuuint32_t>(heads), 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
   auto one = [&](CUtensorMap* m, void* base) {
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   return one(k, c.k_data) && one(v, c.v_data);

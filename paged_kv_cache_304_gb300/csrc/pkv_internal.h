@@ -201,10 +201,11 @@ struct AttnQ4Args {
   void* workspace;
   Q4Cache cache;
 };
-// Tensor maps over a layer's codes seen as rows of 128 bytes, for boxes of
-// `rows` of them with the 128-byte swizzle (16-byte chunk c of row i at chunk
-// c ^ (i % 8)).
-bool encode_q4_maps(const Q4Cache& c, int rows, CUtensorMap* k, CUtensorMap* v);
+// Tensor maps over a layer's codes (num_blocks, 256, Hkv, 64 bytes) for boxes of
+// `tokens` tokens of one block and `heads` kv heads, laid out in shared memory as
+// [head][token][64 bytes] with the 64-byte swizzle (16-byte chunk c of token t at
+// chunk c ^ ((t / 2) % 4)).
+bool encode_q4_maps(const Q4Cache& c, int tokens, int heads, CUtensorMap* k, CUtensorMap* v);
 size_t decode_q4_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_sms);
 size_t prefill_q4_workspace_bytes(int total_q, int num_seqs, int max_seqlen_q, int max_seqlen_k, int num_q_heads,
                                   int num_kv_heads, int num_sms);
