@@ -67,7 +67,7 @@ struct Shape<1> {
 };
 template <>
 struct Shape<2> {
-  static constexpr int kConsumers = 8, kRegsLaunch = 168, kRegsConsumer = 224, kRegsProducer = 56;
+  static constexpr int kConsumers = 8, kRegsLaunch = 168, kRegsConsumer = 216, kRegsProducer = 64;
 };
 template <int NT>
 constexpr int threads_of() {
@@ -359,35 +359,32 @@ __device__ void consumer(const Params& p, const Smem& sm) {
       if (!mbar_wait(&sm.qfull[qs], (units / kQSlots) & 1u, &g_err_decode_q4)) return;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float x[32];
+        // Two passes over the 64 bytes (the largest element first) keep few registers live.
+        const bool real = g + 8 * n < p.G;
+        const uint32_t src = smem_u32(sm.qbuf) + qs * p.q_slot_bytes +
+                             (h * p.G + (real ? g + 8 * n : 0)) * (kHeadDim * 2) + c * 64;
         float top = 0.f;
-        if (g + 8 * n < p.G) {
-          const uint4* src = reinterpret_cast<const uint4*>(sm.qbuf + qs * p.q_slot_bytes +
-                                                            (h * p.G + g + 8 * n) * (kHeadDim * 2) + c * 64);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 a = src[i];
-            const uint32_t ww[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[8 * i + 2 * j] = q4::bf_lo(ww[j]);
-              x[8 * i + 2 * j + 1] = q4::bf_hi(ww[j]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const uint4 a = lds128(src + 16 * i);
+          top = fmax3(top, fmax3(fabsf(q4::bf_lo(a.x)), fabsf(q4::bf_hi(a.x)), fabsf(q4::bf_lo(a.y))),
+                      fmax3(fabsf(q4::bf_hi(a.y)), fabsf(q4::bf_lo(a.z)), fabsf(q4::bf_hi(a.z))));
+          top = fmax3(top, fabsf(q4::bf_lo(a.w)), fabsf(q4::bf_hi(a.w)));
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^(14 - e) for a largest element in [2^e, 2^(e+1))
+        // 2^(14 - e) for a largest element in [2^e, 2^(e+1)); 0 for a head that is not there
         const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 15), 254);
-        const float f = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+        const float f = real ? __uint_as_float(static_cast<uint32_t>(268 - ex) << 23) : 0.f;
         const float inv = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) qb[n][j] = pack_f16x2(x[2 * j] * f, x[2 * j + 1] * f);
+        for (int i = 0; i < 4; ++i) {
+          const uint4 a = lds128(src + 16 * i);
+          qb[n][4 * i] = pack_f16x2(q4::bf_lo(a.x) * f, q4::bf_hi(a.x) * f);
+          qb[n][4 * i + 1] = pack_f16x2(q4::bf_lo(a.y) * f, q4::bf_hi(a.y) * f);
+          qb[n][4 * i + 2] = pack_f16x2(q4::bf_lo(a.z) * f, q4::bf_hi(a.z) * f);
+          qb[n][4 * i + 3] = pack_f16x2(q4::bf_lo(a.w) * f, q4::bf_hi(a.w) * f);
+        }
         sl[n][0] = p.sl2 * __shfl_sync(0xffffffffu, inv, 8 * c);
         sl[n][1] = p.sl2 * __shfl_sync(0xffffffffu, inv, 8 * c + 4);
         m[n][0] = m[n][1] = kLowest;
@@ -401,33 +398,20 @@ __device__ void consumer(const Params& p, const Smem& sm) {
     const int left = hd.hi - hd.t0;  // real tokens of the 32
     if (left > 0) {
       const uint32_t sb = ring + stage * p.stage_bytes;
-      uint4 kw[4];       // K rows tau(g) + 8i
-      uint32_t ks[4];    // their two scales
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        kw[i] = lds128(sb + ko + i * 512);
-        ks[i] = lds_u16(sb + kso + i * 8 * srow);
-      }
       // S^T = K Q^T for the two steps of 16 tokens
       float s[NT][2][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int u = 0; u < 2; ++u) {
+        const uint4 ka = lds128(sb + ko + u * 1024), kb = lds128(sb + ko + u * 1024 + 512);  // rows tau(g), + 8
+        const uint32_t fa = q4::dec_scale2(lds_u16(sb + kso + u * 16 * srow));
+        const uint32_t fb = q4::dec_scale2(lds_u16(sb + kso + u * 16 * srow + 8 * srow));
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int n = 0; n < NT; ++n) s[n][u][0] = s[n][u][1] = s[n][u][2] = s[n][u][3] = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[n][u][i] = 0.f;
-      uint32_t f[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = q4::dec_scale2(ks[i]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint4 ka = kw[2 * u], kb = kw[2 * u + 1];
+        for (int i = 0; i < 4; ++i) {
           const uint32_t wa = i == 0 ? ka.x : i == 1 ? ka.y : i == 2 ? ka.z : ka.w;
           const uint32_t wb = i == 0 ? kb.x : i == 1 ? kb.y : i == 2 ? kb.z : kb.w;
-          const uint32_t ea = i < 2 ? dup_lo(f[2 * u]) : dup_hi(f[2 * u]);
-          const uint32_t eb = i < 2 ? dup_lo(f[2 * u + 1]) : dup_hi(f[2 * u + 1]);
+          const uint32_t ea = i < 2 ? dup_lo(fa) : dup_hi(fa), eb = i < 2 ? dup_lo(fb) : dup_hi(fb);
           uint32_t a[4], b[4];
           q4::dec8(wa, a);
           q4::dec8(wb, b);
@@ -443,17 +427,6 @@ __device__ void consumer(const Params& p, const Smem& sm) {
           }
         }
       }
-      uint2 vw[8];       // V words of tokens tau(2c), tau(2c + 1), + 8, ...
-      uint32_t vs[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        vw[2 * i] = lds64(sb + va + i * 512);
-        vw[2 * i + 1] = lds64(sb + vb + i * 512);
-        vs[2 * i] = lds_u8(sb + vsa + i * 8 * srow);
-        vs[2 * i + 1] = lds_u8(sb + vsb + i * 8 * srow);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.empty[stage]);
       const bool ragged = left < kStepTokens;
       uint32_t pb[NT][2][2];
 #pragma unroll
@@ -502,21 +475,28 @@ __device__ void consumer(const Params& p, const Smem& sm) {
         }
       }
       // O^T += V^T P^T
-      if (ragged) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (8 * i + ta >= left) vs[2 * i] = 0;
-          if (8 * i + tb >= left) vs[2 * i + 1] = 0;
-        }
-      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t e01 = q4::dec_scale2(vs[4 * u] | vs[4 * u + 1] << 8);
-        const uint32_t e23 = q4::dec_scale2(vs[4 * u + 2] | vs[4 * u + 3] << 8);
+        // V words and scales of tokens tau(2c), tau(2c + 1), + 8
+        const uint2 v0 = lds64(sb + va + u * 1024), v1 = lds64(sb + vb + u * 1024);
+        const uint2 v2 = lds64(sb + va + u * 1024 + 512), v3 = lds64(sb + vb + u * 1024 + 512);
+        uint32_t s0 = lds_u8(sb + vsa + u * 16 * srow), s1 = lds_u8(sb + vsb + u * 16 * srow);
+        uint32_t s2 = lds_u8(sb + vsa + (u * 16 + 8) * srow), s3 = lds_u8(sb + vsb + (u * 16 + 8) * srow);
+        if (u == 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.empty[stage]);
+        }
+        if (ragged) {
+          if (16 * u + ta >= left) s0 = 0;
+          if (16 * u + tb >= left) s1 = 0;
+          if (16 * u + ta + 8 >= left) s2 = 0;
+          if (16 * u + tb + 8 >= left) s3 = 0;
+        }
+        const uint32_t e01 = q4::dec_scale2(s0 | s1 << 8), e23 = q4::dec_scale2(s2 | s3 << 8);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const uint32_t a0 = half ? vw[4 * u].y : vw[4 * u].x, a1 = half ? vw[4 * u + 1].y : vw[4 * u + 1].x;
-          const uint32_t a2 = half ? vw[4 * u + 2].y : vw[4 * u + 2].x, a3 = half ? vw[4 * u + 3].y : vw[4 * u + 3].x;
+          const uint32_t a0 = half ? v0.y : v0.x, a1 = half ? v1.y : v1.x;
+          const uint32_t a2 = half ? v2.y : v2.x, a3 = half ? v3.y : v3.x;
           const uint32_t kLow = 0x0f0f0f0fu;
           uint32_t ev0[4], od0[4], ev1[4], od1[4];
           q4::dec8((a0 & kLow) | ((a1 << 4) & ~kLow), ev0);
