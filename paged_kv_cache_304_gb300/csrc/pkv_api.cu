@@ -103,6 +103,18 @@ bool encode_q4_maps(const Q4Cache& c, int tokens, int heads, CUtensorMap* k, CUt
   return one(k, c.k_data) && one(v, c.v_data);
 }
 
+bool encode_q4_query_map(const uint16_t* q, int total_q, int num_q_heads, int log2_heads, CUtensorMap* m) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(num_q_heads), static_cast<cuuint64_t>(total_q)};
+  cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(num_q_heads) * kHeadDim * 2};
+  cuuint32_t box[3] = {64, 1u << log2_heads, 128u >> log2_heads};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(q), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 // Shape checks shared by the two attention calls.

@@ -209,6 +209,9 @@ bool encode_q4_maps(const Q4Cache& c, int tokens, int heads, CUtensorMap* k, CUt
 size_t decode_q4_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int num_sms);
 size_t prefill_q4_workspace_bytes(int total_q, int num_seqs, int max_seqlen_q, int max_seqlen_k, int num_q_heads,
                                   int num_kv_heads, int num_sms);
+// Tensor map over q [total_q, Hq, 128] bf16 for boxes of 64 dims x 2^log2_heads
+// heads x 128 / 2^log2_heads tokens with the 128-byte swizzle.
+bool encode_q4_query_map(const uint16_t* q, int total_q, int num_q_heads, int log2_heads, CUtensorMap* m);
 cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream);
 

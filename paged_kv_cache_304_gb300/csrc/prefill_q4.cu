@@ -1,6 +1,39 @@
-// prefill_q4.cu -- packed prompts against the 4-bit cache (plain form: a warp per
-// query row and head walks the visible keys one at a time).
+// prefill_q4.cu -- varlen causal GQA prefill attention over the 4-bit cache, on the
+// 5th-generation tensor cores (tcgen05).
+//
+// Bound by the tensor pipe: 4 x 128 flops per (query row, visible key) and head.
+// The tensor cores have no product of a 16-bit operand with block-scaled 4-bit
+// codes, so K and V tiles are turned into fp16 on the way into shared memory.
+//
+// One CTA = one 128-row query tile of one sequence for two row groups ("slots"
+// A and B) of the same kv head.  A slot holds 128 tokens of one query head, or,
+// when a sequence's new tokens fit, 128 / 2^k tokens of 2^k heads (row = token *
+// 2^k + head), so that a step of a few tokens does not waste whole tiles.
+// Four warpgroups, registers dealt out again with setmaxnreg:
+// * warps 0-3: Q loads by TMA; one MMA-issuing thread per slot.
+// * warps 4-7 (slot A), 8-11 (slot B): first turn the slot's Q tile into fp16 in
+//   place, thread r its row r, scaled by a power of two so that the row's largest
+//   element is in [2^14, 2^15); then the softmax, thread r on row r (TMEM lane
+//   r), with the power of two undone in the row's softmax scale.
+// * warps 12-15: thread i turns token i of the 128-token K and V tiles into fp16:
+//   64 bytes of codes and 8 scales, fetched a tile ahead into registers, become
+//   128 dims (one conversion and one multiplication per two dims, exact) written
+//   in the 128-byte swizzle that the matrix descriptors expect.
+// Tensor memory: S (128 columns, handed from slot to slot), P_A | P_B (64 each,
+// packed fp16), O_A | O_B (128 each); the slots ping-pong so that one slot's
+// products run while the other's softmax does.
+// Slots of the cache behind a sequence's end hold anything, NaN scales among
+// it: their scores are masked and their V rows written as zeros.  A V group that
+// holds a NaN is written as zeros as well and the NaN goes into its token's K row
+// instead, so that it reaches the queries that see the token and no others.
+// With too few tiles for the GPU the keys are split over several CTAs, which
+// leave (max, sum, unnormalised output) triples for a combine kernel.
+// Every wait is bounded (two seconds); on timeout the CTA flags
+// PKV_DEVERR_WAIT_TIMEOUT, lets the copies and MMAs it has already issued
+// complete, frees its tensor memory and returns.
 #include <cuda_runtime.h>
+
+#include <cfloat>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -11,76 +44,674 @@ namespace {
 
 __device__ unsigned int g_err_prefill_q4;
 
-struct Acc {
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+constexpr int kTileM = 128;  // query rows per slot
+constexpr int kTileN = 128;  // keys per K/V tile
+constexpr int kKStages = 3;
+constexpr int kVStages = 2;
+constexpr int kThreads = 512;
+// Registers a thread: the launch gives 128, the warpgroups' shares add up to
+// 4 x 128 (64 + 176 + 176 + 96).
+constexpr int kRegsLaunch = 128, kRegsCtl = 64, kRegsSoftmax = 176, kRegsDequant = 96;
+static_assert(kRegsCtl + 2 * kRegsSoftmax + kRegsDequant == 4 * kRegsLaunch, "register split must match the launch");
+constexpr uint32_t kTileBytes = kTileN * kHeadDim * 2;  // 32 KiB: one Q, K or V tile in 16 bits
+constexpr uint32_t kHalfBytes = kTileBytes / 2;         // one 64-dim half
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kIdescS = tc::idesc_f16_f32(kTileM, kTileN, 0);     // B = K tile, K-major
+constexpr uint32_t kIdescPV = tc::idesc_f16_f32(kTileM, kHeadDim, 1);  // B = V tile, N-major
+
+struct Params {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const int32_t* tables;
+  uint16_t* out;
+  Q4Cache c;
+  float* ws_o;    // [split, token, head, 128], only with several splits
+  float2* ws_ml;  // [split, token, head] (row max in log2 units, row sum)
+  int32_t maxb, Hq, Hkv, G, groups, npairs, total_q, max_q, max_k, splits;
+  int32_t log2_heads;  // heads of a slot: 2^log2_heads
+  float sl2;           // scale * k_scale * log2(e)
 };
+
+struct Smem {
+  uint8_t* q;   // 2 tiles
+  uint8_t* k0;  // kKStages tiles
+  uint8_t* v0;  // kVStages tiles
+  uint64_t* q_full;   // [2 slots]: bf16 Q has landed
+  uint64_t* q_ready;  // [2 slots]: Q is fp16
+  uint64_t* k_full;   // [kKStages]
+  uint64_t* k_empty;  // [kKStages]
+  uint64_t* v_full;   // [kVStages]
+  uint64_t* v_empty;  // [kVStages]
+  uint64_t* s_full;   // [2 slots]
+  uint64_t* s_free;   // [2 slots]: the shared S columns may take this slot's next S
+  uint64_t* p_full;   // [2 slots]
+  uint64_t* pv_done;  // [2 slots]
+  uint64_t* o_done;   // [2 slots]
+  uint64_t* drain;    // [2 slots]
+  uint32_t* tmem_base;
+};
+
+__device__ __forceinline__ Smem carve(uint8_t* base) {
+  Smem s;
+  s.q = base;
+  s.k0 = base + 2 * kTileBytes;
+  s.v0 = s.k0 + kKStages * kTileBytes;
+  s.q_full = reinterpret_cast<uint64_t*>(s.v0 + kVStages * kTileBytes);
+  s.q_ready = s.q_full + 2;
+  s.k_full = s.q_ready + 2;
+  s.k_empty = s.k_full + kKStages;
+  s.v_full = s.k_empty + kKStages;
+  s.v_empty = s.v_full + kVStages;
+  s.s_full = s.v_empty + kVStages;
+  s.s_free = s.s_full + 2;
+  s.p_full = s.s_free + 2;
+  s.pv_done = s.p_full + 2;
+  s.o_done = s.pv_done + 2;
+  s.drain = s.o_done + 2;
+  s.tmem_base = reinterpret_cast<uint32_t*>(s.drain + 2);
+  return s;
+}
+
+constexpr size_t kSmemBytes = 1024 + (2 + kKStages + kVStages) * kTileBytes + 32 * sizeof(uint64_t) + 16;
+static_assert(kSmemBytes <= 232448, "shared memory per block");
+
+// Wait used only after a timeout, to let work this CTA already issued (bulk
+// copies, MMAs) finish before its shared and tensor memory are given up:
+// bounded (100 ms), reports nothing (the timeout has been reported).
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > 100000000ull) return;
+}
+
+// Matrix descriptors are built once per CTA; a k-step only adds a constant to
+// the 16-byte address field in the low bits (the addresses stay below
+// 256 KiB, so the add never carries out of the field, nor out of the low
+// word: one 32-bit add, the high word kept as it is).  Rebuilding the 64-bit
+// descriptor for every instruction made the single issuing thread, not the
+// tensor pipe, the limit.
+__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) {
+  return (d & 0xFFFFFFFF00000000ull) | static_cast<uint32_t>(static_cast<uint32_t>(d) + (bytes >> 4));
+}
+
+// S = Q K^T: A = Q tile, B = K tile, both K-major (dims contiguous) with the
+// 128-byte swizzle; k-step kk selects 32 bytes of a 64-dim half.
+__device__ __forceinline__ void issue_s(uint32_t d, uint64_t qdesc, uint64_t kdesc) {
+#pragma unroll
+  for (int kk = 0; kk < kHeadDim / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+    tc::mma_ss(d, desc_add(qdesc, off), desc_add(kdesc, off), kIdescS, kk > 0);
+  }
+}
+
+// O += P V with P (128 x 128 keys, packed fp16) in tensor memory at `p_tmem`
+// and V (keys x dims, dims contiguous) in shared memory: 64-dim halves are
+// 16 KiB apart (leading offset), 8-key groups 1 KiB apart (stride offset).
+__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p_tmem, uint64_t vdesc, bool acc) {
+#pragma unroll
+  for (int kk = 0; kk < kTileN / 16; ++kk)
+    tc::mma_ts(o, p_tmem + kk * 8, desc_add(vdesc, kk * 2048), kIdescPV, (acc || kk > 0) ? 1u : 0u);
+}
+
+// ------------------------------------------------------------------ dequantisation
+struct Packed {
+  uint4 d[4];  // 64 bytes of codes
+  uint2 s;     // 8 scales
+};
+
+// Bytes of w that are e4m3 NaNs, as 0xff.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
+// Token `i` of 128-token tile j of K or V, kv head g.
+__device__ __forceinline__ void fetch(const Params& p, const int32_t* table, int j, bool is_v, int i, int g, int len,
+                                      Packed& o) {
+  int phys = __ldg(table + (j >> 1));
+  if (phys < 0 || phys >= p.c.num_blocks) {
+    atomicOr(&g_err_prefill_q4, PKV_DEVERR_BLOCK_RANGE);
+    phys = 0;
+  }
+  const int64_t row = (static_cast<int64_t>(phys) * kBlockSize + (j & 1) * kTileN + i) * p.Hkv + g;
+  const uint4* d = reinterpret_cast<const uint4*>((is_v ? p.c.v_data : p.c.k_data) + row * q4::kRowBytes);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) o.d[u] = __ldg(d + u);
+  const uint2 vs = __ldg(reinterpret_cast<const uint2*>(p.c.v_scales + row * q4::kRowScales));
+  const uint32_t n0 = nan_bytes(vs.x), n1 = nan_bytes(vs.y);
+  if (is_v) {
+    const bool real = kTileN * j + i < len;
+    o.s = make_uint2(real ? vs.x & ~n0 : 0u, real ? vs.y & ~n1 : 0u);
+  } else {
+    o.s = __ldg(reinterpret_cast<const uint2*>(p.c.k_scales + row * q4::kRowScales));
+    if (n0 | n1) o.s = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+}
+
+// Its 128 dims into row i of the tile at shared address `dst`.
+__device__ __forceinline__ void expand(const Packed& x, uint32_t dst, int i) {
+  const uint32_t row = dst + i * 128;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    // scales of groups 2u, 2u + 1
+    const uint32_t two = (u < 2 ? x.s.x : x.s.y) >> (16 * (u & 1));
+    const uint32_t f = q4::dec_scale2(two & 0xffffu);
+    const uint32_t f0 = __byte_perm(f, 0, 0x1010), f1 = __byte_perm(f, 0, 0x3232);
+    const uint32_t w[4] = {x.d[u].x, x.d[u].y, x.d[u].z, x.d[u].w};
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      uint32_t o[4];
+      q4::dec8(w[v], o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = q4::hmul2(o[e], v < 2 ? f0 : f1);
+      const int chunk = 4 * u + v;  // 8 dims
+      const uint32_t a = row + (chunk >> 3) * kHalfBytes + (((chunk & 7) ^ (i & 7)) << 4);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                   : "memory");
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_q4_kernel(const __grid_constant__ CUtensorMap qmap, const Params p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int g = blockIdx.x / p.npairs;  // kv head
+  const int pair = blockIdx.x - g * p.npairs;
+  const bool has_b = 2 * pair + 1 < p.groups;  // slot B: the next group of heads
+  const int seq = blockIdx.y;
+  const int rank = blockIdx.z / p.splits, split = blockIdx.z - rank * p.splits;
+  const int q0 = __ldg(p.cu_q + seq), q1 = __ldg(p.cu_q + seq + 1);
+  const int k0 = __ldg(p.cu_k + seq), k1 = __ldg(p.cu_k + seq + 1);
+  const int n = q1 - q0, L = k1 - k0;
+  const int c = L - n;
+  if (n <= 0) return;
+  if (c < 0 || L > static_cast<long long>(p.maxb) * kBlockSize || q1 > p.total_q || q0 < 0 || n > p.max_q ||
+      L > p.max_k) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0) atomicOr(&g_err_prefill_q4, PKV_DEVERR_LEN_RANGE);
+    return;
+  }
+  const int tile_tokens = kTileM >> p.log2_heads;
+  const int ntiles = (n + tile_tokens - 1) / tile_tokens;
+  if (rank >= ntiles) return;
+  const int m = ntiles - 1 - rank;  // heaviest tile first
+  const int tok0 = tile_tokens * m;                       // first new token of the tile
+  const int kv_end = c + min(tok0 + tile_tokens, n);      // keys 0 .. kv_end-1 are visible to some row
+  const int nkv_all = (kv_end + kTileN - 1) / kTileN;
+  const int j0 = static_cast<int>(static_cast<int64_t>(nkv_all) * split / p.splits);
+  const int nkv = static_cast<int>(static_cast<int64_t>(nkv_all) * (split + 1) / p.splits) - j0;  // this CTA's K/V tiles
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  const Smem sm = carve(base);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head0 = g * p.G + ((2 * pair) << p.log2_heads);  // first query head of slot A
+
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&qmap);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&sm.k_full[i], 4);
+      mbar_init(&sm.k_empty[i], has_b ? 2 : 1);  // released by each slot's S
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&sm.v_full[i], 4);
+      mbar_init(&sm.v_empty[i], has_b ? 2 : 1);  // released by each slot's P V
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_ready[i], 4);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.s_free[i], 4);
+      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.pv_done[i], 1);
+      mbar_init(&sm.o_done[i], 1);
+      mbar_init(&sm.drain[i], 1);
+    }
+    fence_barrier_init();
+    if (nkv > 0) {
+      for (int s = 0; s < (has_b ? 2 : 1); ++s) {
+        mbar_arrive_expect_tx(&sm.q_full[s], kTileBytes);
+        const int hs = head0 + (s << p.log2_heads);
+        tma_load_3d(sm.q + s * kTileBytes, &qmap, &sm.q_full[s], 0, hs, q0 + tok0);
+        tma_load_3d(sm.q + s * kTileBytes + kHalfBytes, &qmap, &sm.q_full[s], 64, hs, q0 + tok0);
+      }
+    }
+  }
+  if (warp == 1) {
+    tc::alloc(sm.tmem_base, kTmemCols);
+    tc::relinquish();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *sm.tmem_base;
+  // columns: S 0-127, P_A 128-191, P_B 192-255, O_A 256-383, O_B 384-511
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    if (lane == 0 && nkv > 0 && (warp == 1 || (warp == 2 && has_b))) {
+      // -------------------------------------------------------- MMA issue
+      // One issuing thread per slot: an issuing thread stays blocked while its
+      // MMAs queue behind the tensor pipe, so one slot's waits overlap the
+      // other slot's MMAs.
+      const int slot = warp - 1;
+      const uint64_t qd = desc_add(tc::smem_desc_sw128(smem_u32(sm.q), 16, 1024), slot * kTileBytes);
+      const uint64_t kd0 = tc::smem_desc_sw128(smem_u32(sm.k0), 16, 1024);
+      const uint64_t vd0 = tc::smem_desc_sw128(smem_u32(sm.v0), kHalfBytes, 1024);
+      const uint32_t sT = tmem, pX = tmem + 128 + 64 * slot, oX = tmem + 256 + 128 * slot;
+      // The S columns are handed over S_A(0), S_B(0), S_A(1), ...: S_X(j)
+      // waits for s_free[X] phase j - 1 (slot A) or j (slot B), completed
+      // when the other slot (or, with one slot, this one) has read its S.
+      bool ok = mbar_wait(&sm.q_ready[slot], 0, &g_err_prefill_q4) && mbar_wait(&sm.k_full[0], 0, &g_err_prefill_q4);
+      if (ok && slot == 1) ok = mbar_wait(&sm.s_free[1], 0, &g_err_prefill_q4);
+      if (ok) {
+        tc::fence_after();
+        issue_s(sT, qd, kd0);
+        tc::commit(&sm.s_full[slot]);
+        tc::commit(&sm.k_empty[0]);
+      }
+      for (int j = 0; j < nkv && ok; ++j) {
+        const int sv = j % kVStages;
+        const bool more = j + 1 < nkv;
+        const int st1 = (j + 1) % kKStages;
+        if (more) {
+          if (!mbar_wait(&sm.s_free[slot], (slot == 0 ? j : j + 1) & 1, &g_err_prefill_q4) ||
+              !mbar_wait(&sm.k_full[st1], ((j + 1) / kKStages) & 1, &g_err_prefill_q4)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after();
+          issue_s(sT, qd, desc_add(kd0, st1 * kTileBytes));
+          tc::commit(&sm.s_full[slot]);
+          tc::commit(&sm.k_empty[st1]);
+        }
+        if (!mbar_wait(&sm.p_full[slot], j & 1, &g_err_prefill_q4) ||
+            !mbar_wait(&sm.v_full[sv], (j / kVStages) & 1, &g_err_prefill_q4)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        issue_pv(oX, pX, desc_add(vd0, sv * kTileBytes), j > 0);
+        tc::commit(&sm.pv_done[slot]);
+        if (!more) tc::commit(&sm.o_done[slot]);
+        tc::commit(&sm.v_empty[sv]);
+      }
+      if (!ok) {
+        // A wait gave up: every MMA this thread issued has completed once
+        // this commit arrives, so tensor memory can be freed after it.
+        tc::commit(&sm.drain[slot]);
+        drain_wait(&sm.drain[slot], 0);
+      }
+    }
+    if (lane == 0 && nkv > 0 && warp == 0) {
+      // The Q copies land before the CTA may end, whatever the other warps do.
+      drain_wait(&sm.q_full[0], 0);
+      if (has_b) drain_wait(&sm.q_full[1], 0);
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int slot = warp >= 8 ? 1 : 0;
+    if (slot == 0 || has_b) {
+      // -------------------------------------------------------- softmax + epilogue
+      const int wq = warp & 3;
+      const int r = wq * 32 + lane;  // tile row = TMEM lane
+      const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
+      const uint32_t s_addr = tmem + lane_bits;                   // shared S columns
+      const uint32_t p_addr = tmem + 128 + slot * 64 + lane_bits;  // this slot's P
+      const uint32_t o_addr = tmem + 256 + slot * 128 + lane_bits;
+      const int tok = tok0 + (r >> p.log2_heads);            // new token of this row
+      const int lim_row = c + tok - kTileN * j0;             // last visible key of this row, from tile j0 on
+      uint8_t* stage = sm.q + slot * kTileBytes;
+      float m_ref = -INFINITY, l = 0.f, sl = 0.f;
+      bool ok = nkv > 0;
+      if (ok) ok = mbar_wait(&sm.q_full[slot], 0, &g_err_prefill_q4);
+      if (ok) {
+        // Row r to fp16 in place, its largest element scaled to [2^14, 2^15).
+        uint32_t w[64];
+        float top = 0.f;
+#pragma unroll
+        for (int cc = 0; cc < 16; ++cc) {
+          const uint4 a = *reinterpret_cast<const uint4*>(stage + (cc >> 3) * kHalfBytes + r * 128 +
+                                                          (((cc & 7) ^ (r & 7)) << 4));
+          w[4 * cc] = a.x;
+          w[4 * cc + 1] = a.y;
+          w[4 * cc + 2] = a.z;
+          w[4 * cc + 3] = a.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 64; ++i) top = fmax3(top, fabsf(q4::bf_lo(w[i])), fabsf(q4::bf_hi(w[i])));
+        const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 15), 254);
+        const float f = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+        sl = p.sl2 * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+#pragma unroll
+        for (int cc = 0; cc < 16; ++cc) {
+          uint4 a;
+          a.x = pack_f16x2(q4::bf_lo(w[4 * cc]) * f, q4::bf_hi(w[4 * cc]) * f);
+          a.y = pack_f16x2(q4::bf_lo(w[4 * cc + 1]) * f, q4::bf_hi(w[4 * cc + 1]) * f);
+          a.z = pack_f16x2(q4::bf_lo(w[4 * cc + 2]) * f, q4::bf_hi(w[4 * cc + 2]) * f);
+          a.w = pack_f16x2(q4::bf_lo(w[4 * cc + 3]) * f, q4::bf_hi(w[4 * cc + 3]) * f);
+          *reinterpret_cast<uint4*>(stage + (cc >> 3) * kHalfBytes + r * 128 + (((cc & 7) ^ (r & 7)) << 4)) = a;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_ready[slot]);
+      }
+      for (int j = 0; j < nkv && ok; ++j) {
+        if (!mbar_wait(&sm.s_full[slot], j & 1, &g_err_prefill_q4)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        // causal mask: key 128 j + x is visible iff x <= lim.  Only warps that
+        // hold a diagonal row take the masked path; the mask of a 32-key
+        // chunk is a 32-bit word (bit x set iff key x of the chunk is visible).
+        const int lim = lim_row - kTileN * j;
+        const bool wdiag = __any_sync(0xffffffffu, lim < kTileN - 1);
+        float s[128];
+        tc::ld32(s_addr + 0, s + 0);
+        tc::ld32(s_addr + 32, s + 32);
+        tc::ld32(s_addr + 64, s + 64);
+        tc::ld32(s_addr + 96, s + 96);
+        tc::wait_ld();
+        // S is in registers: let the MMA warp reuse the S columns.
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.s_free[(slot == 0 && has_b) ? 1 : 0]);
+        if (wdiag) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int nv = lim - 32 * q + 1;  // visible keys in chunk q
+            const uint32_t vm = nv >= 32 ? 0xffffffffu : (nv <= 0 ? 0u : ((1u << nv) - 1u));
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!((vm >> x) & 1u)) s[32 * q + x] = -INFINITY;
+          }
+        }
+        float mx[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mx[u] = s[u];
+#pragma unroll
+        for (int x = 8; x < 128; x += 2) mx[(x >> 1) & 7] = fmax3(mx[(x >> 1) & 7], s[x], s[x + 1]);
+        const float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+        const float m_new = fmaxf(m_ref, mt * sl);
+        float alpha = 1.f;
+        if (m_new > m_ref + 8.f) {
+          alpha = fast_exp2(m_ref - m_new);  // 0 on the first tile (m_ref = -inf)
+          m_ref = m_new;
+        }
+        // A row that has seen no key yet (a split behind the diagonal) keeps -inf.
+        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+        // p = 2^(s * sl - m) <= 2^8, packed to fp16 pairs
+        float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sl2 = make_float2(sl, sl), nmu = make_float2(-mu, -mu);
+        uint32_t pk[64];
+#pragma unroll
+        for (int x = 0; x < 128; x += 2) {
+          const float2 a = ffma2(make_float2(s[x], s[x + 1]), sl2, nmu);
+          const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+          rs[(x >> 1) & 3] = fadd2(rs[(x >> 1) & 3], e);
+          pk[x >> 1] = pack_f16x2(e.x, e.y);
+        }
+        // P_X(j-1) must be consumed (and O_X stable) before P_X(j) is stored.
+        if (j > 0) {
+          if (!mbar_wait(&sm.pv_done[slot], (j - 1) & 1, &g_err_prefill_q4)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after();
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) tc::st32u(p_addr + 32 * q, pk + 32 * q);
+        // O_X is stable here: PV_X(j-1) has completed (pv_done above).
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            float o[32];
+            tc::ld32(o_addr + cc * 32, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] *= alpha;
+            tc::st32(o_addr + cc * 32, o);
+          }
+        }
+        const float2 r01 = fadd2(rs[0], rs[1]), r23 = fadd2(rs[2], rs[3]);
+        const float2 rt = fadd2(r01, r23);
+        l = l * alpha + (rt.x + rt.y);
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[slot]);
+      }
+      const int head = head0 + (slot << p.log2_heads) + (r & ((1 << p.log2_heads) - 1));
+      const bool real = tok < n && head < (g + 1) * p.G;
+      if (p.splits > 1) {
+        // Partial result of this split; one without keys leaves a zero sum.
+        const int64_t at = (static_cast<int64_t>(split) * p.total_q + q0 + tok) * p.Hq + head;
+        if (nkv > 0 && ok) ok = mbar_wait(&sm.o_done[slot], 0, &g_err_prefill_q4);
+        if (real) p.ws_ml[at] = make_float2(l > 0.f || l != l ? m_ref : -FLT_MAX, ok ? l : 0.f);
+        if (nkv > 0 && ok) {
+          tc::fence_after();
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            float o[32];
+            tc::ld32(o_addr + cc * 32, o);
+            tc::wait_ld();
+            if (real) {
+              float4* dst = reinterpret_cast<float4*>(p.ws_o + at * kHeadDim + cc * 32);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            }
+          }
+        }
+      } else if (ok && mbar_wait(&sm.o_done[slot], 0, &g_err_prefill_q4)) {
+        tc::fence_after();
+        const float inv = p.c.v_scale / l;
+        // Stage the bf16 row in this slot's Q buffer (free: o_done implies that
+        // every MMA that reads it has completed), swizzled like a Q row, then
+        // write whole rows: 16 lanes a row, 16 bytes a lane.
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float o[64];
+          tc::ld32(o_addr + 64 * hh, o);
+          tc::ld32(o_addr + 64 * hh + 32, o + 32);
+          tc::wait_ld();
+#pragma unroll
+          for (int c8 = 0; c8 < 8; ++c8) {
+            const float* v = o + 8 * c8;
+            uint4 w;
+            w.x = pack_bf16x2(v[0] * inv, v[1] * inv);
+            w.y = pack_bf16x2(v[2] * inv, v[3] * inv);
+            w.z = pack_bf16x2(v[4] * inv, v[5] * inv);
+            w.w = pack_bf16x2(v[6] * inv, v[7] * inv);
+            *reinterpret_cast<uint4*>(stage + hh * kHalfBytes + r * 128 + ((c8 ^ (r & 7)) << 4)) = w;
+          }
+        }
+        __syncwarp();
+        const int ch = lane & 15;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int tr = 32 * wq + 2 * i + (lane >> 4);  // tile row written by this lane
+          const int tt = tok0 + (tr >> p.log2_heads);
+          const int th = head0 + (slot << p.log2_heads) + (tr & ((1 << p.log2_heads) - 1));
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + (ch >> 3) * kHalfBytes + tr * 128 +
+                                                          (((ch & 7) ^ (tr & 7)) << 4));
+          if (tt < n && th < (g + 1) * p.G)
+            *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(q0 + tt) * p.Hq + th) * kHeadDim + ch * 8) = w;
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
+    // ---------------------------------------------------------- dequantisation
+    // Order K(0), K(1), V(0), K(2), V(1), ...: the MMA warps need K(j+1) (for
+    // the next S) before V(j) (for P V of j).
+    const int i = threadIdx.x - 384;  // token of the tile
+    const int32_t* table = p.tables + static_cast<int64_t>(seq) * p.maxb;
+    const int steps = 2 * nkv;
+    auto item = [&](int s, int* j) {  // true: V
+      if (s == 0) {
+        *j = 0;
+        return false;
+      }
+      if (s == steps - 1) {
+        *j = nkv - 1;
+        return true;
+      }
+      const bool v = (s & 1) == 0;
+      *j = (s + 1) / 2 - (v ? 1 : 0);
+      return v;
+    };
+    auto put = [&](int s, const Packed& x) {
+      int j;
+      const bool v = item(s, &j);
+      const int st = v ? j % kVStages : j % kKStages;
+      const uint32_t par = ((v ? j / kVStages : j / kKStages) & 1) ^ 1;
+      if (!mbar_wait(v ? &sm.v_empty[st] : &sm.k_empty[st], par, &g_err_prefill_q4)) return false;
+      expand(x, smem_u32(v ? sm.v0 + st * kTileBytes : sm.k0 + st * kTileBytes), i);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v ? &sm.v_full[st] : &sm.k_full[st]);
+      return true;
+    };
+    auto get = [&](int s, Packed& x) {
+      int j;
+      const bool v = item(s, &j);
+      fetch(p, table, j0 + j, v, i, g, L, x);
+    };
+    if (steps > 0) {
+      Packed a, b;
+      get(0, a);
+      for (int s = 0; s < steps; s += 2) {
+        get(s + 1, b);
+        if (!put(s, a)) break;
+        if (s + 2 < steps) get(s + 2, a);
+        if (!put(s + 1, b)) break;
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 1) tc::dealloc(tmem, kTmemCols);
+}
+
+// Join the splits' partial results: one warp per (token, head), lane i dims
+// 4i .. 4i+3.  Tokens that no valid sequence owns are left alone.
+constexpr int kCombineWarps = 4;
+
+__global__ void __launch_bounds__(32 * kCombineWarps) prefill_q4_combine_kernel(const Params p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int seq = blockIdx.y, lane = threadIdx.x & 31;
+  const int q0 = __ldg(p.cu_q + seq), n = __ldg(p.cu_q + seq + 1) - q0;
+  const int L = __ldg(p.cu_k + seq + 1) - __ldg(p.cu_k + seq);
+  if (n <= 0 || L < n || L > static_cast<long long>(p.maxb) * kBlockSize || q0 + n > p.total_q || q0 < 0 ||
+      n > p.max_q || L > p.max_k)
+    return;
+  const int64_t pairs = static_cast<int64_t>(n) * p.Hq;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5); i < pairs;
+       i += static_cast<int64_t>(gridDim.x) * kCombineWarps) {
+    const int64_t at = static_cast<int64_t>(q0) * p.Hq + i, step = static_cast<int64_t>(p.total_q) * p.Hq;
+    float M = -FLT_MAX;
+    for (int s = 0; s < p.splits; ++s) M = fmaxf(M, p.ws_ml[at + s * step].x);
+    float lsum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < p.splits; ++s) {
+      const float2 ml = p.ws_ml[at + s * step];
+      if (ml.y == 0.f) continue;  // no key of this split is visible: nothing was written
+      const float w = fast_exp2(ml.x - M);
+      const float4 v = *reinterpret_cast<const float4*>(p.ws_o + (at + s * step) * kHeadDim + 4 * lane);
+      lsum += w * ml.y;
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    }
+    const float inv = p.c.v_scale / lsum;
+    *reinterpret_cast<uint2*>(p.out + at * kHeadDim + 4 * lane) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
+
+// How a call is laid out, from sizes that the host knows.
+struct Plan {
+  int log2_heads, groups, npairs, tiles, splits;
+};
+
+Plan plan_for(int num_seqs, int max_q, int max_k, int hq, int hkv, int num_sms) {
+  Plan a;
+  const int group = (hq + hkv - 1) / hkv;
+  // Several heads in a slot when all new tokens of a sequence fit with them.
+  a.log2_heads = 0;
+  while ((2 << a.log2_heads) <= group && static_cast<int64_t>(max_q) << (a.log2_heads + 1) <= kTileM) ++a.log2_heads;
+  a.groups = (group + (1 << a.log2_heads) - 1) >> a.log2_heads;
+  a.npairs = (a.groups + 1) / 2;
+  const int tokens = kTileM >> a.log2_heads;
+  a.tiles = (max_q + tokens - 1) / tokens;
+  // Fewer CTAs than SMs: split the keys, at least four tiles (512 keys) to a split.
+  const int64_t ctas = static_cast<int64_t>(hkv) * a.npairs * num_seqs * a.tiles;
+  const int64_t most = std::max<int64_t>(1, (max_k + kTileN - 1) / kTileN / 4);
+  a.splits = ctas > 0 ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / ctas, most))) : 1;
+  return a;
+}
+
+size_t ml_bytes(const Plan& a, int total_q, int hq) {
+  return align256(static_cast<size_t>(a.splits) * total_q * hq * sizeof(float2));
+}
 
 }  // namespace
 
-// Lane i holds dims 4i .. 4i+3 of the query; keys 0 .. len-1 of the sequence.
-__device__ void attend_row_q4(const Q4Cache& c, const uint16_t* q, uint16_t* out, const int32_t* table, int len,
-                              int kvh, float sl2, unsigned int* err) {
-  const int lane = threadIdx.x & 31;
-  const uint2 w = *reinterpret_cast<const uint2*>(q + 4 * lane);
-  const float x[4] = {q4::bf_lo(w.x), q4::bf_hi(w.x), q4::bf_lo(w.y), q4::bf_hi(w.y)};
-  Acc a;
-  for (int t = 0; t < len; ++t) {
-    int b = __ldg(table + t / kBlockSize);
-    if (b < 0 || b >= c.num_blocks) {
-      if (lane == 0) atomicOr(err, PKV_DEVERR_BLOCK_RANGE);
-      b = 0;
-    }
-    const int64_t row = (static_cast<int64_t>(b) * kBlockSize + t % kBlockSize) * c.num_kv_heads + kvh;
-    uint32_t h[4];
-    q4::dec8(*reinterpret_cast<const uint16_t*>(c.k_data + row * 64 + 2 * lane), h);
-    const float ks = q4::dec_scale(c.k_scales[row * 8 + (lane >> 2)]);
-    float s = ks * (x[0] * q4::half_lo(h[0]) + x[1] * q4::half_hi(h[0]) + x[2] * q4::half_lo(h[1]) +
-                    x[3] * q4::half_hi(h[1]));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= sl2;
-    const float m = fmaxf(a.m, s);
-    const float alpha = fast_exp2(a.m - m), p = fast_exp2(s - m);
-    a.m = m;
-    a.l = a.l * alpha + p;
-    q4::dec8(*reinterpret_cast<const uint16_t*>(c.v_data + row * 64 + 2 * lane), h);
-    const float vs = p * q4::dec_scale(c.v_scales[row * 8 + (lane >> 2)]);
-    a.o[0] = a.o[0] * alpha + vs * q4::half_lo(h[0]);
-    a.o[1] = a.o[1] * alpha + vs * q4::half_hi(h[0]);
-    a.o[2] = a.o[2] * alpha + vs * q4::half_lo(h[1]);
-    a.o[3] = a.o[3] * alpha + vs * q4::half_hi(h[1]);
-  }
-  const float inv = len > 0 ? c.v_scale / a.l : 0.f;
-  *reinterpret_cast<uint2*>(out + 4 * lane) =
-      make_uint2(pack_bf16x2(a.o[0] * inv, a.o[1] * inv), pack_bf16x2(a.o[2] * inv, a.o[3] * inv));
+size_t prefill_q4_workspace_bytes(int total_q, int num_seqs, int max_seqlen_q, int max_seqlen_k, int num_q_heads,
+                                  int num_kv_heads, int num_sms) {
+  const Plan a = plan_for(num_seqs, max_seqlen_q, max_seqlen_k, num_q_heads, num_kv_heads, num_sms);
+  if (a.splits <= 1) return 256;
+  return ml_bytes(a, total_q, num_q_heads) +
+         static_cast<size_t>(a.splits) * total_q * num_q_heads * kHeadDim * sizeof(float);
 }
 
-__global__ void __launch_bounds__(128) prefill_q4_kernel(const AttnQ4Args p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t pair = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int row = static_cast<int>(pair / p.num_q_heads), h = static_cast<int>(pair % p.num_q_heads);
-  const int i = blockIdx.y;
-  const int q0 = p.cu_seqlens_q[i], q1 = p.cu_seqlens_q[i + 1];
-  const int n = q1 - q0, len = p.cu_seqlens_k[i + 1] - p.cu_seqlens_k[i];
-  if (n <= 0) return;
-  if (len < n || len > static_cast<long long>(p.max_blocks_per_seq) * kBlockSize || q1 > p.total_q || q0 < 0 ||
-      n > p.max_seqlen_q || len > p.max_seqlen_k) {
-    if (pair == 0 && threadIdx.x == 0) atomicOr(&g_err_prefill_q4, PKV_DEVERR_LEN_RANGE);
-    return;
+cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
+  const Plan pl = plan_for(a.num_seqs, a.max_seqlen_q, a.max_seqlen_k, a.num_q_heads, a.cache.num_kv_heads, num_sms);
+  // The warpgroups' requests for registers can only be met if the kernel was
+  // built with exactly the launch's share per thread.
+  static std::atomic<int> regs_checked{0};
+  if (!regs_checked.load(std::memory_order_acquire)) {
+    cudaFuncAttributes fa{};
+    const cudaError_t e = cudaFuncGetAttributes(&fa, prefill_q4_kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
+    regs_checked.store(1, std::memory_order_release);
   }
-  if (row >= n) return;
-  const int64_t at = (static_cast<int64_t>(q0 + row) * p.num_q_heads + h) * kHeadDim;
-  attend_row_q4(p.cache, p.q + at, p.out + at, p.block_tables + static_cast<int64_t>(i) * p.max_blocks_per_seq,
-                len - n + row + 1, h / (p.num_q_heads / p.cache.num_kv_heads),
-                p.scale * p.cache.k_scale * 1.4426950408889634f, &g_err_prefill_q4);
-}
-
-size_t prefill_q4_workspace_bytes(int, int, int, int, int, int, int) { return 256; }
-
-cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int, cudaStream_t stream) {
-  const int64_t pairs = static_cast<int64_t>(a.max_seqlen_q) * a.num_q_heads;
-  return launch_pdl(prefill_q4_kernel, dim3(static_cast<unsigned>((pairs + 3) / 4), a.num_seqs), dim3(128), 0, stream, a);
+  CUtensorMap qmap;
+  if (!encode_q4_query_map(a.q, a.total_q, a.num_q_heads, pl.log2_heads, &qmap)) return cudaErrorUnknown;
+  Params p = {};
+  p.cu_q = a.cu_seqlens_q;
+  p.cu_k = a.cu_seqlens_k;
+  p.tables = a.block_tables;
+  p.out = a.out;
+  p.c = a.cache;
+  p.ws_ml = static_cast<float2*>(a.workspace);
+  p.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + ml_bytes(pl, a.total_q, a.num_q_heads));
+  p.maxb = a.max_blocks_per_seq;
+  p.Hq = a.num_q_heads;
+  p.Hkv = a.cache.num_kv_heads;
+  p.G = p.Hq / p.Hkv;
+  p.groups = pl.groups;
+  p.npairs = pl.npairs;
+  p.total_q = a.total_q;
+  p.max_q = a.max_seqlen_q;
+  p.max_k = a.max_seqlen_k;
+  p.splits = pl.splits;
+  p.log2_heads = pl.log2_heads;
+  p.sl2 = a.scale * a.cache.k_scale * 1.4426950408889634f;
+  static std::atomic<int> smem_set[kMaxDevices];
+  cudaError_t e = ensure_dyn_smem(prefill_q4_kernel, kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(prefill_q4_kernel, dim3(p.Hkv * pl.npairs, a.num_seqs, pl.tiles * pl.splits), dim3(kThreads),
+                 kSmemBytes, stream, qmap, p);
+  if (e != cudaSuccess || pl.splits <= 1) return e;
+  const int64_t pairs = static_cast<int64_t>(a.max_seqlen_q) * p.Hq;
+  const unsigned x = static_cast<unsigned>(std::min<int64_t>((pairs + kCombineWarps - 1) / kCombineWarps, 4096));
+  return launch_pdl(prefill_q4_combine_kernel, dim3(x, a.num_seqs), dim3(32 * kCombineWarps), 0, stream, p);
 }
 
 PKV_DEFINE_READ_ERROR(read_error_prefill_q4, g_err_prefill_q4)
