@@ -410,41 +410,60 @@ def sample_exponential_race(logits: torch.Tensor, temperatures: torch.Tensor, se
     return out
 
 
-def _launch(fn: str, dev: torch.device, *args) -> None:
-    """Call `fn` of the library with `dev` current and its current stream as the last argument."""
-    lib = load()
-    if dev.index == torch.cuda.current_device():
-        _check(fn, getattr(lib, fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
+# The helpers of the newer calls.  Each call costs the host a few microseconds, so
+# the checks read every property of a tensor once and spell out what is wrong only
+# when something is.
+_BF16, _I32, _Tensor = torch.bfloat16, torch.int32, torch.Tensor
+_raw_stream, _raw_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _launch(fn: str, dev: int, *args) -> None:
+    """Call `fn` of the library with device `dev` current and its current stream as the last argument."""
+    f = getattr(_lib or load(), fn)
+    if _raw_device() == dev:
+        status = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(fn, getattr(lib, fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
+            status = f(*args, _raw_stream(dev))
+    if status:
+        raise PkvError(fn, status)
 
 
-def _same_device(dev: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _wrong(t, name: str, dtype, dev: int | None, want: str):
+    """Why `t` is not a tensor of this type on this device (dev None: any), contiguous or shaped as wanted."""
+    _dev(t, name, dtype)
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{name} must be {want}")
 
 
-def _ints(dev: torch.device, **tensors) -> None:
-    """Contiguous int32 tensors on `dev`."""
-    for name, t in tensors.items():
-        _dev(t, name, torch.int32)
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _ints(t: torch.Tensor, name: str, dev: int, *shape) -> int:
+    """Pointer of a contiguous int32 tensor on `dev`; a None in `shape` fits any size."""
+    if (not isinstance(t, _Tensor) or t.dtype != _I32 or t.get_device() != dev or not t.is_contiguous()
+            or len(t.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
+        _wrong(t, name, _I32, dev, f"contiguous, {list(shape)}")
+    return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, name: str, heads: int | None = None, head_dim: int = 128):
-    """[N, heads, head_dim] bf16 with contiguous rows; returns (N, heads, token stride)."""
-    _dev(t, name, torch.bfloat16)
-    if t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [N, {'heads' if heads is None else heads}, {head_dim}]")
-    n, h = int(t.shape[0]), int(t.shape[1])
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != head_dim):
-        raise ValueError(f"{name} must have contiguous rows")
-    return n, h, t.stride(0) if n > 1 else h * head_dim
+def _rows(t: torch.Tensor, name: str, dev: int | None = None, tokens: int | None = None, heads: int | None = None):
+    """(pointer, tokens, heads, token stride) of [N, heads, 128] bf16 with contiguous rows."""
+    if not isinstance(t, _Tensor) or t.dtype != _BF16 or not t.is_cuda or (dev is not None and t.get_device() != dev):
+        _wrong(t, name, _BF16, dev, "")
+    shape, stride = t.shape, t.stride()
+    if (len(shape) != 3 or shape[2] != 128 or stride[2] != 1 or (shape[1] > 1 and stride[1] != 128)
+            or (tokens is not None and shape[0] != tokens) or (heads is not None and shape[1] != heads)):
+        raise ValueError(f"{name} must be [{'N' if tokens is None else tokens}, "
+                         f"{'heads' if heads is None else heads}, 128] with contiguous rows")
+    n, h = shape[0], shape[1]
+    return t.data_ptr(), n, h, stride[0] if n > 1 else h * 128
+
+
+def _dense(t: torch.Tensor, name: str, shape, dev: int) -> int:
+    """Pointer of a contiguous bf16 tensor of this shape on `dev`."""
+    if (not isinstance(t, _Tensor) or t.dtype != _BF16 or t.get_device() != dev or t.shape != shape
+            or not t.is_contiguous()):
+        _wrong(t, name, _BF16, dev, f"contiguous, {list(shape)}")
+    return t.data_ptr()
 
 
 def device_error(clear: bool = True) -> list[str]:

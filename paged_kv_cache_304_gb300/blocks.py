@@ -15,24 +15,21 @@ from . import _dev, _ints, _launch
 
 
 def _pool(block_tables, context_lens, ref_count):
+    """(device, S, max_blocks, num_blocks, pointers of the three)."""
     _dev(ref_count, "ref_count", torch.int32)
-    dev = ref_count.device
-    _ints(dev, block_tables=block_tables, context_lens=context_lens, ref_count=ref_count)
-    if block_tables.dim() != 2 or context_lens.shape != (block_tables.shape[0],) or ref_count.dim() != 1:
-        raise ValueError("block_tables must be [S, max_blocks], context_lens [S] and ref_count [num_blocks]")
-    return dev, int(block_tables.shape[0]), int(block_tables.shape[1]), int(ref_count.shape[0])
+    dev = ref_count.get_device()
+    rp = _ints(ref_count, "ref_count", dev, None)
+    tp = _ints(block_tables, "block_tables", dev, None, None)
+    s, maxb = block_tables.shape
+    return dev, s, maxb, ref_count.shape[0], tp, _ints(context_lens, "context_lens", dev, s), rp
 
 
-def _outputs(out, names, shapes, dev):
+def _outputs(out, names, shapes, device, dev):
     if out is None:
-        return tuple(torch.empty(s, dtype=torch.int32, device=dev) for s in shapes)
-    if len(out) != len(names):
+        out = tuple(torch.empty(s, dtype=torch.int32, device=device) for s in shapes)
+    elif len(out) != len(names):
         raise ValueError(f"out must hold {', '.join(names)}")
-    for t, n, s in zip(out, names, shapes):
-        _ints(dev, **{n: t})
-        if tuple(t.shape) != s:
-            raise ValueError(f"{n} must be of shape {s}")
-    return tuple(out)
+    return tuple(out), [_ints(t, n, dev, *s) for t, n, s in zip(out, names, shapes)]
 
 
 def fork_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, parents: torch.Tensor,
@@ -43,21 +40,19 @@ def fork_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, parents:
     free one of its own and a pair of copy_src, copy_dst for copy_blocks.  `out`
     may hold the four tensors to write into.
     """
-    dev, s, maxb, nb = _pool(block_tables, context_lens, ref_count)
-    _ints(dev, parents=parents)
-    if parents.dim() != 1:
-        raise ValueError("parents must be [n]")
-    n = int(parents.shape[0])
-    out = _outputs(out, ("child_tables", "child_lens", "copy_src", "copy_dst"), ((n, maxb), (n,), (n,), (n,)), dev)
-    _launch("pkv_fork_blocks", dev, block_tables.data_ptr(), context_lens.data_ptr(), s, maxb, parents.data_ptr(), n,
-            ref_count.data_ptr(), nb, *(t.data_ptr() for t in out))
+    dev, s, maxb, nb, tp, lp, rp = _pool(block_tables, context_lens, ref_count)
+    pp = _ints(parents, "parents", dev, None)
+    n = parents.shape[0]
+    out, ptrs = _outputs(out, ("child_tables", "child_lens", "copy_src", "copy_dst"), ((n, maxb), (n,), (n,), (n,)),
+                         ref_count.device, dev)
+    _launch("pkv_fork_blocks", dev, tp, lp, s, maxb, pp, n, rp, nb, *ptrs)
     return out
 
 
 def free_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, ref_count: torch.Tensor) -> None:
     """Give back the blocks of every row: each loses one reference in ref_count."""
-    dev, s, maxb, nb = _pool(block_tables, context_lens, ref_count)
-    _launch("pkv_free_blocks", dev, block_tables.data_ptr(), context_lens.data_ptr(), s, maxb, ref_count.data_ptr(), nb)
+    dev, s, maxb, nb, tp, lp, rp = _pool(block_tables, context_lens, ref_count)
+    _launch("pkv_free_blocks", dev, tp, lp, s, maxb, rp, nb)
 
 
 def compact_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, ref_count: torch.Tensor, out=None):
@@ -68,11 +63,10 @@ def compact_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, ref_c
     copy_blocks.  `out` may hold the five tensors to write into, the first two
     being block_tables and ref_count themselves if wanted.
     """
-    dev, s, maxb, nb = _pool(block_tables, context_lens, ref_count)
-    out = _outputs(out, ("new_tables", "new_ref_count", "copy_src", "copy_dst", "num_moves"),
-                   ((s, maxb), (nb,), (nb // 2,), (nb // 2,), (1,)), dev)
-    _launch("pkv_compact_blocks", dev, block_tables.data_ptr(), context_lens.data_ptr(), s, maxb,
-            ref_count.data_ptr(), nb, *(t.data_ptr() for t in out))
+    dev, s, maxb, nb, tp, lp, rp = _pool(block_tables, context_lens, ref_count)
+    out, ptrs = _outputs(out, ("new_tables", "new_ref_count", "copy_src", "copy_dst", "num_moves"),
+                         ((s, maxb), (nb,), (nb // 2,), (nb // 2,), (1,)), ref_count.device, dev)
+    _launch("pkv_compact_blocks", dev, tp, lp, s, maxb, rp, nb, *ptrs)
     return out
 
 
@@ -84,14 +78,11 @@ def copy_blocks(cache: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, block
     block's contents.  src, dst: int32 [n]; pairs of -1 are skipped.
     """
     _dev(cache, "cache")
-    dev = cache.device
-    _ints(dev, src=src, dst=dst)
-    if not cache.is_contiguous() or not 0 <= block_dim < cache.dim():
+    dev, shape = cache.get_device(), cache.shape
+    if not cache.is_contiguous() or not 0 <= block_dim < len(shape):
         raise ValueError("cache must be contiguous with block_dim one of its dims")
-    if src.dim() != 1 or dst.shape != src.shape:
-        raise ValueError("src and dst must be [n]")
-    shape = tuple(int(x) for x in cache.shape)
+    sp = _ints(src, "src", dev, None)
+    n = src.shape[0]
     planes, nb = math.prod(shape[:block_dim]), shape[block_dim]
     size = math.prod(shape[block_dim + 1:]) * cache.element_size()
-    _launch("pkv_copy_blocks", dev, cache.data_ptr(), planes, nb * size, nb, size, src.data_ptr(), dst.data_ptr(),
-            int(src.shape[0]))
+    _launch("pkv_copy_blocks", dev, cache.data_ptr(), planes, nb * size, nb, size, sp, _ints(dst, "dst", dev, n), n)

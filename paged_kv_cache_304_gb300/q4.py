@@ -11,7 +11,7 @@ import math
 
 import torch
 
-from . import _dev, _ints, _launch, _rows, _same_device, load
+from . import _dense, _dev, _ints, _launch, _rows, load
 
 HEAD_DIM = 128
 GROUP = 16
@@ -50,12 +50,14 @@ class Q4Cache:
                            (k_scales, "k_scales", HEAD_DIM // GROUP), (v_scales, "v_scales", HEAD_DIM // GROUP)):
             if tuple(t.shape) != (nb, bs, hkv, last) or not t.is_contiguous():
                 raise ValueError(f"{n} must be contiguous [{nb}, {bs}, {hkv}, {last}]")
-        _same_device(k_data.device, k_scales=k_scales, v_data=v_data, v_scales=v_scales)
+            if t.device != k_data.device:
+                raise ValueError(f"{n} is on {t.device}, expected {k_data.device}")
         self.k_data, self.k_scales, self.v_data, self.v_scales = k_data, k_scales, v_data, v_scales
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         if not (self.k_scale > 0 and self.v_scale > 0 and math.isfinite(self.k_scale) and math.isfinite(self.v_scale)):
             raise ValueError("tensor scales must be finite and positive")
         self.num_blocks, self.block_size, self.num_kv_heads, self.device = nb, bs, hkv, k_data.device
+        self._index = k_data.get_device()
         self._struct = _Struct(k_data.data_ptr(), k_scales.data_ptr(), v_data.data_ptr(), v_scales.data_ptr(),
                                self.k_scale, self.v_scale, nb, bs, hkv, HEAD_DIM)
         self._ref = ctypes.addressof(self._struct)
@@ -78,47 +80,44 @@ def _cache(c) -> Q4Cache:
 
 def kv_cache_write_q4(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, cache: Q4Cache) -> None:
     """Quantise k, v [N, Hkv, 128] (bf16, rows may be strided) into the cache at slot_mapping [N]; -1 is skipped."""
-    dev = _cache(cache).device
-    n, _, ks = _rows(k, "k", cache.num_kv_heads)
-    nv, _, vs = _rows(v, "v", cache.num_kv_heads)
-    _ints(dev, slot_mapping=slot_mapping)
-    _same_device(dev, k=k, v=v)
-    if nv != n or slot_mapping.shape != (n,):
-        raise ValueError("k, v and slot_mapping must have the same number of tokens")
-    _launch("pkv_kv_cache_write_q4", dev, k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), n, cache._ref)
+    dev, hkv = _cache(cache)._index, cache.num_kv_heads
+    kp, n, _, ks = _rows(k, "k", dev, None, hkv)
+    vp, _, _, vs = _rows(v, "v", dev, n, hkv)
+    _launch("pkv_kv_cache_write_q4", dev, kp, ks, vp, vs, _ints(slot_mapping, "slot_mapping", dev, n), n, cache._ref)
 
 
 def kv_cache_read_q4(cache: Q4Cache, slots: torch.Tensor, k_out: torch.Tensor | None = None,
                      v_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """The rows that slots [N] (int32) hold, as bf16 k, v [N, Hkv, 128]; slot -1 gives zeros."""
-    dev = _cache(cache).device
-    _ints(dev, slots=slots)
-    if slots.dim() != 1:
-        raise ValueError("slots must be [N]")
-    shape = (int(slots.shape[0]), cache.num_kv_heads, HEAD_DIM)
-    k_out, v_out = _out(k_out, "k_out", shape, dev), _out(v_out, "v_out", shape, dev)
-    _launch("pkv_kv_cache_read_q4", dev, cache._ref, slots.data_ptr(), shape[0], k_out.data_ptr(), v_out.data_ptr())
+    dev = _cache(cache)._index
+    sp = _ints(slots, "slots", dev, None)
+    shape = (slots.shape[0], cache.num_kv_heads, HEAD_DIM)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    _launch("pkv_kv_cache_read_q4", dev, cache._ref, sp, shape[0], _dense(k_out, "k_out", shape, dev),
+            _dense(v_out, "v_out", shape, dev))
     return k_out, v_out
-
-
-def _out(t, name, shape, dev):
-    if t is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _dev(t, name, torch.bfloat16)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"{name} must be a contiguous bf16 tensor of shape {tuple(shape)} on {dev}")
-    return t
 
 
 def _workspace(n: int, device) -> torch.Tensor:
     return torch.empty(max(256, n), dtype=torch.uint8, device=device)
 
 
-def _workspace_arg(t: torch.Tensor, dev):
-    _dev(t, "workspace")
-    if not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+def _workspace_arg(t: torch.Tensor, dev: int):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
+        _dev(t, "workspace")
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _queries(q: torch.Tensor, dev: int):
+    """(pointer, rows, heads) of contiguous [N, Hq, 128] bf16."""
+    p, n, hq, stride = _rows(q, "q", dev)
+    if stride != hq * HEAD_DIM:
+        raise ValueError("q must be contiguous")
+    return p, n, hq
 
 
 def decode_q4_workspace(batch: int, num_q_heads: int, num_kv_heads: int, device) -> torch.Tensor:
@@ -132,24 +131,17 @@ def paged_attn_decode_q4(q: torch.Tensor, cache: Q4Cache, context_lens: torch.Te
                          scale: float, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                          max_context_len: int | None = None) -> torch.Tensor:
     """Decode attention over the 4-bit cache; arguments as in paged_attn_decode."""
-    dev = _cache(cache).device
-    _dev(q, "q", torch.bfloat16)
-    _same_device(dev, q=q)
-    _ints(dev, context_lens=context_lens, block_tables=block_tables)
-    if q.dim() != 3 or q.shape[2] != HEAD_DIM or not q.is_contiguous():
-        raise ValueError("q must be contiguous [B, Hq, 128]")
-    b, hq = int(q.shape[0]), int(q.shape[1])
-    if block_tables.dim() != 2 or block_tables.shape[0] != b or context_lens.shape != (b,):
-        raise ValueError("block_tables must be [B, max_blocks] and context_lens [B]")
-    out = _out(out, "out", q.shape, dev)
+    dev = _cache(cache)._index
+    qp, b, hq = _queries(q, dev)
+    tp = _ints(block_tables, "block_tables", dev, b, None)
+    if out is None:
+        out = torch.empty_like(q)
     if workspace is None:
-        workspace = decode_q4_workspace(b, hq, cache.num_kv_heads, dev)
-    wp, wb = _workspace_arg(workspace, dev)
-    maxb = int(block_tables.shape[1])
-    if max_context_len is None:
-        max_context_len = maxb * cache.block_size
-    _launch("pkv_paged_attn_decode_q4", dev, q.data_ptr(), cache._ref, context_lens.data_ptr(),
-            block_tables.data_ptr(), maxb, b, hq, int(max_context_len), float(scale), out.data_ptr(), wp, wb)
+        workspace = decode_q4_workspace(b, hq, cache.num_kv_heads, cache.device)
+    maxb = block_tables.shape[1]
+    _launch("pkv_paged_attn_decode_q4", dev, qp, cache._ref, _ints(context_lens, "context_lens", dev, b), tp, maxb, b,
+            hq, maxb * cache.block_size if max_context_len is None else max_context_len, scale,
+            _dense(out, "out", q.shape, dev), *_workspace_arg(workspace, dev))
     return out
 
 
@@ -166,22 +158,17 @@ def paged_attn_prefill_q4(q: torch.Tensor, cache: Q4Cache, cu_seqlens_q: torch.T
                           block_tables: torch.Tensor, scale: float, max_seqlen_q: int, max_seqlen_k: int,
                           out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Varlen causal prefill attention over the 4-bit cache; arguments as in paged_attn_prefill."""
-    dev = _cache(cache).device
-    _dev(q, "q", torch.bfloat16)
-    _same_device(dev, q=q)
-    _ints(dev, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, block_tables=block_tables)
-    if q.dim() != 3 or q.shape[2] != HEAD_DIM or not q.is_contiguous():
-        raise ValueError("q must be contiguous [T, Hq, 128]")
-    total, hq = int(q.shape[0]), int(q.shape[1])
-    s = int(cu_seqlens_q.numel()) - 1
-    if (s < 0 or cu_seqlens_q.dim() != 1 or cu_seqlens_k.shape != (s + 1,) or block_tables.dim() != 2
-            or block_tables.shape[0] != s):
-        raise ValueError("cu_seqlens_q and cu_seqlens_k must be [S+1] and block_tables [S, max_blocks]")
-    out = _out(out, "out", q.shape, dev)
+    dev = _cache(cache)._index
+    qp, total, hq = _queries(q, dev)
+    cq = _ints(cu_seqlens_q, "cu_seqlens_q", dev, None)
+    s = cu_seqlens_q.shape[0] - 1
+    if s < 0:
+        raise ValueError("cu_seqlens_q must be [S+1]")
+    if out is None:
+        out = torch.empty_like(q)
     if workspace is None:
-        workspace = prefill_q4_workspace(total, s, int(max_seqlen_q), int(max_seqlen_k), hq, cache.num_kv_heads, dev)
-    wp, wb = _workspace_arg(workspace, dev)
-    _launch("pkv_paged_attn_prefill_q4", dev, q.data_ptr(), cache._ref, cu_seqlens_q.data_ptr(),
-            cu_seqlens_k.data_ptr(), block_tables.data_ptr(), int(block_tables.shape[1]), s, total, int(max_seqlen_q),
-            int(max_seqlen_k), hq, float(scale), out.data_ptr(), wp, wb)
+        workspace = prefill_q4_workspace(total, s, max_seqlen_q, max_seqlen_k, hq, cache.num_kv_heads, cache.device)
+    _launch("pkv_paged_attn_prefill_q4", dev, qp, cache._ref, cq, _ints(cu_seqlens_k, "cu_seqlens_k", dev, s + 1),
+            _ints(block_tables, "block_tables", dev, s, None), block_tables.shape[1], s, total, max_seqlen_q,
+            max_seqlen_k, hq, scale, _dense(out, "out", q.shape, dev), *_workspace_arg(workspace, dev))
     return out

@@ -6,22 +6,18 @@ Argument marshalling only; the contract of each call stands in
 
 from __future__ import annotations
 
-import ctypes
 import math
+import struct
 
 import torch
 
-from . import _cache_dims, _dev, _ints, _launch, _rows, _same_device
+from . import _cache_dims, _dense, _dev, _ints, _launch, _rows, _wrong
 from .q4 import Q4Cache, _cache
 
 HEAD_DIM = 128
-
-
-class _Struct(ctypes.Structure):
-    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("freqs", ctypes.c_void_p),
-                ("positions", ctypes.c_void_p), ("position_axis_stride", ctypes.c_int64), ("eps", ctypes.c_float),
-                ("rope_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("num_axes", ctypes.c_int32),
-                ("sections", ctypes.c_int32 * 3)]
+# pkv_norm_rope: q_weight, k_weight, freqs, positions, position_axis_stride, eps, rope_dim, interleaved, num_axes,
+# sections[3]
+_PACK = struct.Struct("@4Pqf3i3i").pack
 
 
 def rope_frequencies(rope_dim: int, base: float = 10000.0, device="cuda", inv_freq=None) -> torch.Tensor:
@@ -48,42 +44,41 @@ def rope_frequencies(rope_dim: int, base: float = 10000.0, device="cuda", inv_fr
     return torch.tensor(turns, dtype=torch.int64, device=device)
 
 
-def _describe(n, dev, q_weight, k_weight, eps, freqs, positions, interleaved, sections) -> _Struct:
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _dev(t, name, torch.bfloat16)
-            if t.shape != (HEAD_DIM,) or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous [{HEAD_DIM}]")
+def _weight(t, name: str, dev: int) -> int:
+    return 0 if t is None else _dense(t, name, (HEAD_DIM,), dev)
+
+
+def _describe(n, dev, q_weight, k_weight, eps, freqs, positions, interleaved, sections) -> bytes:
+    wq, wk = _weight(q_weight, "q_weight", dev), _weight(k_weight, "k_weight", dev)
     if freqs is None:
-        rot, axes, stride, sections = 0, 1, 0, (0,)
-    else:
-        _dev(freqs, "freqs", torch.int64)
-        _dev(positions, "positions", torch.int32)
-        if freqs.dim() != 1 or not freqs.is_contiguous():
-            raise ValueError("freqs must be contiguous [rope_dim / 2]")
-        rot = 2 * int(freqs.shape[0])
-        if positions.dim() not in (1, 2) or positions.shape[-1] != n or (n > 1 and positions.stride(-1) != 1):
-            raise ValueError("positions must be [N] or [axes, N] with contiguous rows")
-        axes = int(positions.shape[0]) if positions.dim() == 2 else 1
-        stride = positions.stride(0) if positions.dim() == 2 and axes > 1 else 0
-        if sections is None:
-            if axes != 1:
-                raise ValueError("several position axes need sections")
-            sections = (rot // 2,)
-        if len(sections) != axes or axes > 3:
-            raise ValueError("sections must have one entry per position axis (1 to 3)")
-    _same_device(dev, q_weight=q_weight, k_weight=k_weight, freqs=freqs, positions=positions if freqs is not None else None)
-    ptr = [0 if t is None else t.data_ptr() for t in (q_weight, k_weight, freqs, positions if rot else None)]
-    return _Struct(*ptr, stride, float(eps), rot, int(bool(interleaved)), axes, (ctypes.c_int32 * 3)(*sections))
+        return _PACK(wq, wk, 0, 0, 0, eps, 0, bool(interleaved), 1, 0, 0, 0)
+    if (not isinstance(freqs, torch.Tensor) or freqs.dtype != torch.int64 or freqs.get_device() != dev
+            or len(freqs.shape) != 1 or not freqs.is_contiguous()):
+        _wrong(freqs, "freqs", torch.int64, dev, "contiguous [rope_dim / 2]")
+    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or positions.get_device() != dev:
+        _wrong(positions, "positions", torch.int32, dev, "")
+    half = freqs.shape[0]
+    shape, stride = positions.shape, positions.stride()
+    if len(shape) not in (1, 2) or shape[-1] != n or (n > 1 and stride[-1] != 1):
+        raise ValueError("positions must be [N] or [axes, N] with contiguous rows")
+    axes, step = (shape[0], stride[0]) if len(shape) == 2 else (1, 0)
+    if sections is None:
+        if axes != 1:
+            raise ValueError("several position axes need sections")
+        sections = (half,)
+    if len(sections) != axes or axes > 3:
+        raise ValueError("sections must have one entry per position axis (1 to 3)")
+    return _PACK(wq, wk, freqs.data_ptr(), positions.data_ptr(), step if axes > 1 else 0, eps, 2 * half,
+                 bool(interleaved), axes, *sections, *(0,) * (3 - axes))
 
 
-def _q_out(q, t):
-    if t is None:
-        t = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    n, h, stride = _rows(t, "output", int(q.shape[1]))
-    if n != q.shape[0] or t.device != q.device:
-        raise ValueError("an output must be shaped like its input, on the same device")
-    return t, stride
+def _like(t: torch.Tensor, out, name: str, dev: int, n: int, h: int):
+    """An output of [n, h, 128]: (tensor, pointer, token stride)."""
+    if out is None:
+        out = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
+        return out, out.data_ptr(), h * HEAD_DIM
+    p, _, _, stride = _rows(out, name, dev, n, h)
+    return out, p, stride
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight, k_weight, eps: float, freqs, positions,
@@ -97,16 +92,13 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight, k_weight, eps: floa
     pairs (2i, 2i + 1) instead of (i, i + rope_dim/2).  q_out, k_out may be q
     and k themselves.
     """
-    n, hq, qs = _rows(q, "q")
-    nk, hkv, ks = _rows(k, "k")
-    if nk != n:
-        raise ValueError("q and k must have the same number of tokens")
-    _same_device(q.device, k=k)
-    q_out, qos = _q_out(q, q_out)
-    k_out, kos = _q_out(k, k_out)
-    nr = _describe(n, q.device, q_weight, k_weight, eps, freqs, positions, interleaved, sections)
-    _launch("pkv_qk_norm_rope", q.device, q.data_ptr(), qs, k.data_ptr(), ks, n, hq, hkv, HEAD_DIM,
-            ctypes.addressof(nr), q_out.data_ptr(), qos, k_out.data_ptr(), kos)
+    qp, n, hq, qs = _rows(q, "q")
+    dev = q.get_device()
+    kp, _, hkv, ks = _rows(k, "k", dev, n)
+    q_out, qo, qos = _like(q, q_out, "q_out", dev, n, hq)
+    k_out, ko, kos = _like(k, k_out, "k_out", dev, n, hkv)
+    _launch("pkv_qk_norm_rope", dev, qp, qs, kp, ks, n, hq, hkv, HEAD_DIM,
+            _describe(n, dev, q_weight, k_weight, eps, freqs, positions, interleaved, sections), qo, qos, ko, kos)
     return q_out, k_out
 
 
@@ -114,18 +106,17 @@ def qk_norm_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weig
                        positions, slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                        interleaved: bool = False, sections=None, q_out: torch.Tensor | None = None) -> torch.Tensor:
     """qk_norm_rope, with its keys and v [N, Hkv, 128] written into the bf16 caches at slot_mapping; returns q_out."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _dev(t, name, torch.bfloat16)
-    nb, bs, hkv, d = _cache_dims(k_cache)
-    if v_cache.shape != k_cache.shape or not v_cache.is_contiguous():
-        raise ValueError("v_cache must match k_cache")
-    n, hq, qs, ks, vs = _qkv(q, k, v, slot_mapping, hkv)
-    _same_device(q.device, k_cache=k_cache, v_cache=v_cache)
-    q_out, qos = _q_out(q, q_out)
-    nr = _describe(n, q.device, q_weight, k_weight, eps, freqs, positions, interleaved, sections)
-    _launch("pkv_qk_norm_rope_write", q.device, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, n, hq,
-            ctypes.addressof(nr), slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, hkv, d,
-            q_out.data_ptr(), qos)
+    qp, n, hq, qs = _rows(q, "q")
+    dev = q.get_device()
+    _dev(k_cache, "k_cache", torch.bfloat16)
+    shape = nb, bs, hkv, d = _cache_dims(k_cache)
+    kp, _, _, ks = _rows(k, "k", dev, n, hkv)
+    vp, _, _, vs = _rows(v, "v", dev, n, hkv)
+    q_out, qo, qos = _like(q, q_out, "q_out", dev, n, hq)
+    _launch("pkv_qk_norm_rope_write", dev, qp, qs, kp, ks, vp, vs, n, hq,
+            _describe(n, dev, q_weight, k_weight, eps, freqs, positions, interleaved, sections),
+            _ints(slot_mapping, "slot_mapping", dev, n), _dense(k_cache, "k_cache", shape, dev),
+            _dense(v_cache, "v_cache", shape, dev), nb, bs, hkv, d, qo, qos)
     return q_out
 
 
@@ -133,22 +124,12 @@ def qk_norm_rope_write_q4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_w
                           positions, slot_mapping: torch.Tensor, cache: Q4Cache, interleaved: bool = False,
                           sections=None, q_out: torch.Tensor | None = None) -> torch.Tensor:
     """qk_norm_rope, with its keys and v quantised into the 4-bit cache at slot_mapping; returns q_out."""
-    n, hq, qs, ks, vs = _qkv(q, k, v, slot_mapping, _cache(cache).num_kv_heads)
-    if cache.device != q.device:
-        raise ValueError(f"cache is on {cache.device}, expected {q.device}")
-    q_out, qos = _q_out(q, q_out)
-    nr = _describe(n, q.device, q_weight, k_weight, eps, freqs, positions, interleaved, sections)
-    _launch("pkv_qk_norm_rope_write_q4", q.device, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, n, hq,
-            ctypes.addressof(nr), slot_mapping.data_ptr(), cache._ref, q_out.data_ptr(), qos)
+    dev, hkv = _cache(cache)._index, cache.num_kv_heads
+    qp, n, hq, qs = _rows(q, "q", dev)
+    kp, _, _, ks = _rows(k, "k", dev, n, hkv)
+    vp, _, _, vs = _rows(v, "v", dev, n, hkv)
+    q_out, qo, qos = _like(q, q_out, "q_out", dev, n, hq)
+    _launch("pkv_qk_norm_rope_write_q4", dev, qp, qs, kp, ks, vp, vs, n, hq,
+            _describe(n, dev, q_weight, k_weight, eps, freqs, positions, interleaved, sections),
+            _ints(slot_mapping, "slot_mapping", dev, n), cache._ref, qo, qos)
     return q_out
-
-
-def _qkv(q, k, v, slot_mapping, hkv):
-    n, hq, qs = _rows(q, "q")
-    nk, _, ks = _rows(k, "k", hkv)
-    nv, _, vs = _rows(v, "v", hkv)
-    _ints(q.device, slot_mapping=slot_mapping)
-    _same_device(q.device, k=k, v=v)
-    if nk != n or nv != n or slot_mapping.shape != (n,):
-        raise ValueError("q, k, v and slot_mapping must have the same number of tokens")
-    return n, hq, qs, ks, vs

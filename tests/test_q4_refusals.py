@@ -106,13 +106,11 @@ def test_prefill_arguments(lib):
 
 
 def norm(**kw):
+    """A pkv_norm_rope description (bytes, read on the host)."""
     a = dict(q_weight=F, k_weight=F, freqs=F, positions=F, position_axis_stride=0, eps=1e-6, rope_dim=128,
              interleaved=0, num_axes=1, sections=(64, 0, 0))
-    a.update(kw)
-    a["sections"] = (ctypes.c_int32 * 3)(*a["sections"])
-    s = rope._Struct(**a)
-    norm.keep = s
-    return ctypes.addressof(s)
+    *fields, sections = ({**a, **kw}).values()
+    return rope._PACK(*(f or 0 for f in fields), *sections)
 
 
 @pytest.mark.parametrize("bad,status", [
