@@ -437,12 +437,22 @@ def _wrong(t, name: str, dtype, dev: int | None, want: str):
     raise ValueError(f"{name} must be {want}")
 
 
-def _ints(t: torch.Tensor, name: str, dev: int, *shape) -> int:
-    """Pointer of a contiguous int32 tensor on `dev`; a None in `shape` fits any size."""
-    if (not isinstance(t, _Tensor) or t.dtype != _I32 or t.get_device() != dev or not t.is_contiguous()
-            or len(t.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
-        _wrong(t, name, _I32, dev, f"contiguous, {list(shape)}")
-    return t.data_ptr()
+def _ints(t: torch.Tensor, name: str, dev: int, n: int | None = None) -> int:
+    """Pointer of a contiguous int32 [n] on `dev` (n None: any length)."""
+    if isinstance(t, _Tensor) and t.dtype == _I32 and t.get_device() == dev and t.is_contiguous():
+        shape = t.shape
+        if len(shape) == 1 and (n is None or shape[0] == n):
+            return t.data_ptr()
+    return _wrong(t, name, _I32, dev, f"contiguous [{'N' if n is None else n}]")
+
+
+def _table(t: torch.Tensor, name: str, dev: int, rows: int | None = None, width: int | None = None) -> int:
+    """Pointer of a contiguous int32 [rows, width] on `dev` (None: any size)."""
+    if isinstance(t, _Tensor) and t.dtype == _I32 and t.get_device() == dev and t.is_contiguous():
+        shape = t.shape
+        if len(shape) == 2 and (rows is None or shape[0] == rows) and (width is None or shape[1] == width):
+            return t.data_ptr()
+    return _wrong(t, name, _I32, dev, f"contiguous [{'S' if rows is None else rows}, max_blocks]")
 
 
 def _rows(t: torch.Tensor, name: str, dev: int | None = None, tokens: int | None = None, heads: int | None = None):

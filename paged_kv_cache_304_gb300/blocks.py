@@ -11,15 +11,15 @@ import math
 
 import torch
 
-from . import _dev, _ints, _launch
+from . import _dev, _ints, _launch, _table
 
 
 def _pool(block_tables, context_lens, ref_count):
     """(device, S, max_blocks, num_blocks, pointers of the three)."""
     _dev(ref_count, "ref_count", torch.int32)
     dev = ref_count.get_device()
-    rp = _ints(ref_count, "ref_count", dev, None)
-    tp = _ints(block_tables, "block_tables", dev, None, None)
+    rp = _ints(ref_count, "ref_count", dev)
+    tp = _table(block_tables, "block_tables", dev)
     s, maxb = block_tables.shape
     return dev, s, maxb, ref_count.shape[0], tp, _ints(context_lens, "context_lens", dev, s), rp
 
@@ -29,7 +29,7 @@ def _outputs(out, names, shapes, device, dev):
         out = tuple(torch.empty(s, dtype=torch.int32, device=device) for s in shapes)
     elif len(out) != len(names):
         raise ValueError(f"out must hold {', '.join(names)}")
-    return tuple(out), [_ints(t, n, dev, *s) for t, n, s in zip(out, names, shapes)]
+    return tuple(out), [(_ints if len(s) == 1 else _table)(t, n, dev, *s) for t, n, s in zip(out, names, shapes)]
 
 
 def fork_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, parents: torch.Tensor,
@@ -41,7 +41,7 @@ def fork_blocks(block_tables: torch.Tensor, context_lens: torch.Tensor, parents:
     may hold the four tensors to write into.
     """
     dev, s, maxb, nb, tp, lp, rp = _pool(block_tables, context_lens, ref_count)
-    pp = _ints(parents, "parents", dev, None)
+    pp = _ints(parents, "parents", dev)
     n = parents.shape[0]
     out, ptrs = _outputs(out, ("child_tables", "child_lens", "copy_src", "copy_dst"), ((n, maxb), (n,), (n,), (n,)),
                          ref_count.device, dev)
@@ -81,7 +81,7 @@ def copy_blocks(cache: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, block
     dev, shape = cache.get_device(), cache.shape
     if not cache.is_contiguous() or not 0 <= block_dim < len(shape):
         raise ValueError("cache must be contiguous with block_dim one of its dims")
-    sp = _ints(src, "src", dev, None)
+    sp = _ints(src, "src", dev)
     n = src.shape[0]
     planes, nb = math.prod(shape[:block_dim]), shape[block_dim]
     size = math.prod(shape[block_dim + 1:]) * cache.element_size()

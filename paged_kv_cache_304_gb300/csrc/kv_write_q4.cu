@@ -1,10 +1,11 @@
 // kv_write_q4.cu -- scatter K/V rows into the 4-bit cache, and read rows back.
 //
 // Per token and kv head 256 bytes of bf16 become 64 bytes of codes and 8 of
-// scales (the read does the reverse); both are bound by HBM.  A lane owns one
-// group of 16 dims (32 bytes in, 8 + 1 bytes out), eight lanes a head's row, so
-// a group's maximum needs no exchange between lanes and a warp moves four heads
-// at a time.  The slot is read once per warp.
+// scales (the read does the reverse); both are bound by HBM.  One warp moves one
+// token; a lane owns chunks of 8 dims, so that 32 lanes read 512 contiguous bytes
+// and write 128, and a group of 16 is a pair of lanes that exchange their maxima.
+// All of a token's chunks (up to four of K and four of V per lane) are requested
+// before the first is used.
 #include <cuda_runtime.h>
 
 #include "pkv_device.cuh"
@@ -17,6 +18,36 @@ namespace {
 __device__ unsigned int g_err_kv_q4;
 
 constexpr int kWarps = 8;
+constexpr int kChunks = kHeadDim / 8;                        // of a head's row
+static_assert(kMaxKvHeads * kChunks == 4 * 32, "four chunks a lane");
+
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+// Quantise one chunk (its group's other half is lane ^ 1's) and store it as
+// chunk `at` of the cache.
+__device__ __forceinline__ void store_chunk(const uint4& a, float inv, uint8_t* data, uint8_t* scales, int64_t at,
+                                            int lane, bool real) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  float y[8], m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[2 * i] = q4::bf_lo(w[i]) * inv;
+    y[2 * i + 1] = q4::bf_hi(w[i]) * inv;
+    m = q4::max_nan(m, q4::max_nan(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+  }
+  m = q4::max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  const uint32_t sb = q4::group_scale(m);
+  const uint32_t codes = q4::enc8_group(y, sb, m);
+  if (!real) return;
+  *reinterpret_cast<uint32_t*>(data + at * 4) = codes;
+  if (!(lane & 1)) scales[at >> 1] = static_cast<uint8_t>(sb);
+}
 
 __global__ void __launch_bounds__(32 * kWarps)
     kv_write_q4_kernel(const uint16_t* __restrict__ k, int64_t k_stride, const uint16_t* __restrict__ v,
@@ -33,30 +64,39 @@ __global__ void __launch_bounds__(32 * kWarps)
       if (lane == 0) atomicOr(&g_err_kv_q4, PKV_DEVERR_SLOT_RANGE);
       continue;
     }
-    // units: group u of the K row, then of the V row (8 groups a head)
-    const int per = c.num_kv_heads * q4::kRowScales;
-    for (int u = lane; u < 2 * per; u += 32) {
-      const bool is_v = u >= per;
-      const int g = is_v ? u - per : u;
-      const uint4* src = reinterpret_cast<const uint4*>((is_v ? v + t * v_stride : k + t * k_stride) + g * 16);
-      const uint4 a = __ldg(src), b = __ldg(src + 1);
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      const float inv = is_v ? c.v_inv : c.k_inv;
-      float y[16], m = 0.f;
+    const int chunks = c.num_kv_heads * kChunks;
+    const uint4* ks = reinterpret_cast<const uint4*>(k + t * k_stride);
+    const uint4* vs = reinterpret_cast<const uint4*>(v + t * v_stride);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 kr[4], vr[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[2 * i] = q4::bf_lo(w[i]) * inv;
-        y[2 * i + 1] = q4::bf_hi(w[i]) * inv;
-        m = q4::max_nan(m, q4::max_nan(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
-      }
-      const uint32_t sb = q4::group_scale(m);
-      const float sc = q4::dec_scale(sb);
-      const int64_t at = s * per + g;
-      *reinterpret_cast<uint2*>((is_v ? c.v_data : c.k_data) + at * 8) =
-          make_uint2(q4::enc8(y, sc), q4::enc8(y + 8, sc));
-      (is_v ? c.v_scales : c.k_scales)[at] = static_cast<uint8_t>(sb);
+    for (int u = 0; u < 4; ++u) {
+      const bool real = 32 * u + lane < chunks;
+      kr[u] = real ? ld_stream(ks + 32 * u + lane) : zero;
+      vr[u] = real ? ld_stream(vs + 32 * u + lane) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (32 * u >= chunks) break;  // the whole warp
+      const bool real = 32 * u + lane < chunks;
+      const int64_t at = s * chunks + 32 * u + lane;
+      store_chunk(kr[u], c.k_inv, c.k_data, c.k_scales, at, lane, real);
+      store_chunk(vr[u], c.v_inv, c.v_data, c.v_scales, at, lane, real);
     }
   }
+}
+
+// Eight codes over scale byte `sb` as bf16.
+__device__ __forceinline__ uint4 expand_chunk(uint32_t codes, uint32_t sb, float ts) {
+  const uint32_t sh = q4::dec_scale2(sb | sb << 8);
+  uint32_t h[4], o[4];
+  q4::dec8(codes, h);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t p = q4::hmul2(h[i], sh);
+    o[i] = pack_bf16x2(q4::half_lo(p) * ts, q4::half_hi(p) * ts);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Rows of slots[i] back as bf16; slot -1 (and, flagged, a slot outside the
@@ -69,35 +109,27 @@ __global__ void __launch_bounds__(32 * kWarps)
   const int lane = threadIdx.x & 31;
   const int64_t num_slots = static_cast<int64_t>(c.num_blocks) * kBlockSize;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int per = c.num_kv_heads * q4::kRowScales;
+  const int chunks = c.num_kv_heads * kChunks;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < num_tokens; t += step) {
     const int64_t s = __ldg(slots + t);
     const bool ok = s >= 0 && s < num_slots;
     if (!ok && s != -1 && lane == 0) atomicOr(&g_err_kv_q4, PKV_DEVERR_SLOT_RANGE);
-    for (int u = lane; u < 2 * per; u += 32) {
-      const bool is_v = u >= per;
-      const int g = is_v ? u - per : u;
-      uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-      if (ok) {
-        const int64_t at = s * per + g;
-        const uint2 d = *reinterpret_cast<const uint2*>((is_v ? c.v_data : c.k_data) + at * 8);
-        const uint32_t sb = (is_v ? c.v_scales : c.k_scales)[at];
-        const uint32_t sh = q4::dec_scale2(sb | sb << 8);
-        const float ts = is_v ? c.v_scale : c.k_scale;
-        uint32_t h[4];
+    uint32_t kd[4], vd[4], ksb[4], vsb[4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          q4::dec8(half ? d.y : d.x, h);
+    for (int u = 0; u < 4; ++u) {
+      const int64_t at = s * chunks + 32 * u + lane;
+      const bool real = ok && 32 * u + lane < chunks;
+      kd[u] = real ? *reinterpret_cast<const uint32_t*>(c.k_data + at * 4) : 0u;
+      vd[u] = real ? *reinterpret_cast<const uint32_t*>(c.v_data + at * 4) : 0u;
+      ksb[u] = real ? c.k_scales[at >> 1] : 0u;
+      vsb[u] = real ? c.v_scales[at >> 1] : 0u;
+    }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t p = q4::hmul2(h[i], sh);
-            o[4 * half + i] = pack_bf16x2(q4::half_lo(p) * ts, q4::half_hi(p) * ts);
-          }
-        }
-      }
-      uint4* dst = reinterpret_cast<uint4*>((is_v ? v : k) + (t * per + g) * 16);
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    for (int u = 0; u < 4; ++u) {
+      if (32 * u + lane >= chunks) break;
+      const int64_t to = t * chunks + 32 * u + lane;
+      reinterpret_cast<uint4*>(k)[to] = expand_chunk(kd[u], ksb[u], c.k_scale);
+      reinterpret_cast<uint4*>(v)[to] = expand_chunk(vd[u], vsb[u], c.v_scale);
     }
   }
 }

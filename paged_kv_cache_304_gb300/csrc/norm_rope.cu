@@ -27,11 +27,7 @@ namespace {
 
 __device__ unsigned int g_err_norm_rope;
 
-constexpr int kWarps = 8;
-
-struct Row {  // 16 dims of one head in a lane: chunk c0 in 0-7, chunk c1 in 8-15
-  float x[16];
-};
+constexpr int kWarps = 4;
 
 __device__ __forceinline__ void unpack(const uint4& a, float* x) {
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -60,7 +56,7 @@ __device__ __forceinline__ void store_q4(uint8_t* data, uint8_t* scales, int64_t
   }
   m = q4::max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
   const uint32_t sb = q4::group_scale(m);
-  const uint32_t w = q4::enc8(y, q4::dec_scale(sb));
+  const uint32_t w = q4::enc8_group(y, sb, m);
   if (!write) return;
   *reinterpret_cast<uint32_t*>(data + row * q4::kRowBytes + chunk * 4) = w;
   if (!(chunk & 1)) scales[row * q4::kRowScales + (chunk >> 1)] = static_cast<uint8_t>(sb);
@@ -131,20 +127,30 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormRopeAr
         }
       }
     }
+    // Group g's row of this lane, the next one's requested while this one is in work.
+    auto load = [&](int g, uint4& a0, uint4& a1) {
+      const bool is_v = g >= rope_groups;
+      const int head = is_v ? 4 * (g - rope_groups) + sub : 4 * g + sub;
+      a0 = a1 = make_uint4(0u, 0u, 0u, 0u);
+      if (g < g1 && head < (is_v ? p.num_kv_heads : rope_heads)) {
+        const uint16_t* row = is_v ? p.v + t * p.v_stride + head * kHeadDim
+                                   : (head < p.num_q_heads ? p.q + t * p.q_stride + head * kHeadDim
+                                                           : p.k + t * p.k_stride + (head - p.num_q_heads) * kHeadDim);
+        // plain loads: the output may be the input
+        a0 = reinterpret_cast<const uint4*>(row)[c0];
+        a1 = reinterpret_cast<const uint4*>(row)[c1];
+      }
+    };
+    uint4 n0, n1;
+    load(g0, n0, n1);
     for (int g = g0; g < g1; ++g) {
+      uint4 a0 = n0, a1 = n1;
+      load(g + 1, n0, n1);
       const bool is_v = g >= rope_groups;
       const int head = is_v ? 4 * (g - rope_groups) + sub : 4 * g + sub;
       const bool is_q = !is_v && head < p.num_q_heads;
       const int kvh = is_v ? head : head - p.num_q_heads;  // kv head of a K or V row
       const bool real = is_v ? head < p.num_kv_heads : head < rope_heads;
-      uint4 a0 = make_uint4(0u, 0u, 0u, 0u), a1 = a0;
-      if (real) {
-        const uint16_t* row = is_v ? p.v + t * p.v_stride + kvh * kHeadDim
-                                   : (is_q ? p.q + t * p.q_stride + head * kHeadDim
-                                           : p.k + t * p.k_stride + kvh * kHeadDim);
-        a0 = reinterpret_cast<const uint4*>(row)[c0];  // plain loads: the output may be the input
-        a1 = reinterpret_cast<const uint4*>(row)[c1];
-      }
       if (!is_v) {
         float x[16], w[16];
         unpack(a0, x);
@@ -221,7 +227,7 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, int dest, int num_sms, cudaS
   int splits = 1;
   while (splits < groups && static_cast<int64_t>(a.num_tokens) * splits < static_cast<int64_t>(num_sms) * 8) ++splits;
   const int64_t items = static_cast<int64_t>(a.num_tokens) * splits;
-  const int64_t blocks = std::min<int64_t>((items + kWarps - 1) / kWarps, static_cast<int64_t>(num_sms) * 16);
+  const int64_t blocks = std::min<int64_t>((items + kWarps - 1) / kWarps, static_cast<int64_t>(num_sms) * 32);
   const dim3 grid(static_cast<unsigned>(blocks)), block(32 * kWarps);
   switch (dest) {
     case 0: return launch_pdl(norm_rope_kernel<0>, grid, block, 0, stream, a, splits);

@@ -15,6 +15,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <cfloat>
 #include <cstdint>
 
 #include "pkv_device.cuh"
@@ -82,13 +83,32 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // Scale byte of a group whose largest |y| is `amax`.
 __device__ __forceinline__ uint32_t group_scale(float amax) { return enc_scale(__fdiv_rn(amax, 6.f)); }
 
-// Eight codes of eight floats y over scale s (as the float its byte stands for).
-__device__ __forceinline__ uint32_t enc8(const float* y, float s) {
+// Eight codes of eight floats y over scale s (as the float its byte stands for);
+// `r` is 1 / s rounded to nearest.  A code depends on which side of a tie y / s
+// lies, so the quotient is needed correctly rounded (a tie is representable, and
+// a quotient that is none does not round to one): the product y r is corrected
+// with its residual, q + (y - q s) r (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990).  An infinite y is
+// taken as its largest code before.
+__device__ __forceinline__ uint32_t enc8(const float* y, float s, float r) {
   uint32_t w = 0;
   if (s == 0.f) return 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w |= enc2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)) << (8 * i);
+  for (int i = 0; i < 4; ++i) {
+    const float a = y[2 * i] * r, b = y[2 * i + 1] * r;
+    w |= enc2(fmaf(fmaf(-a, s, y[2 * i]), r, a), fmaf(fmaf(-b, s, y[2 * i + 1]), r, b)) << (8 * i);
+  }
   return w;
+}
+
+// Codes of eight floats whose group's scale byte is `sb`.
+__device__ __forceinline__ uint32_t enc8_group(float* y, uint32_t sb, float amax) {
+  if (amax == INFINITY) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(y[i], -FLT_MAX), FLT_MAX);
+  }
+  const float s = dec_scale(sb);
+  return enc8(y, s, __frcp_rn(s));
 }
 
 // bf16 pair word to two floats (exact).

@@ -11,7 +11,7 @@ import math
 
 import torch
 
-from . import _dense, _dev, _ints, _launch, _rows, load
+from . import _dense, _dev, _ints, _launch, _rows, _table, load
 
 HEAD_DIM = 128
 GROUP = 16
@@ -90,7 +90,7 @@ def kv_cache_read_q4(cache: Q4Cache, slots: torch.Tensor, k_out: torch.Tensor | 
                      v_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """The rows that slots [N] (int32) hold, as bf16 k, v [N, Hkv, 128]; slot -1 gives zeros."""
     dev = _cache(cache)._index
-    sp = _ints(slots, "slots", dev, None)
+    sp = _ints(slots, "slots", dev)
     shape = (slots.shape[0], cache.num_kv_heads, HEAD_DIM)
     if k_out is None:
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
@@ -133,7 +133,7 @@ def paged_attn_decode_q4(q: torch.Tensor, cache: Q4Cache, context_lens: torch.Te
     """Decode attention over the 4-bit cache; arguments as in paged_attn_decode."""
     dev = _cache(cache)._index
     qp, b, hq = _queries(q, dev)
-    tp = _ints(block_tables, "block_tables", dev, b, None)
+    tp = _table(block_tables, "block_tables", dev, b)
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
@@ -160,7 +160,7 @@ def paged_attn_prefill_q4(q: torch.Tensor, cache: Q4Cache, cu_seqlens_q: torch.T
     """Varlen causal prefill attention over the 4-bit cache; arguments as in paged_attn_prefill."""
     dev = _cache(cache)._index
     qp, total, hq = _queries(q, dev)
-    cq = _ints(cu_seqlens_q, "cu_seqlens_q", dev, None)
+    cq = _ints(cu_seqlens_q, "cu_seqlens_q", dev)
     s = cu_seqlens_q.shape[0] - 1
     if s < 0:
         raise ValueError("cu_seqlens_q must be [S+1]")
@@ -169,6 +169,6 @@ def paged_attn_prefill_q4(q: torch.Tensor, cache: Q4Cache, cu_seqlens_q: torch.T
     if workspace is None:
         workspace = prefill_q4_workspace(total, s, max_seqlen_q, max_seqlen_k, hq, cache.num_kv_heads, cache.device)
     _launch("pkv_paged_attn_prefill_q4", dev, qp, cache._ref, cq, _ints(cu_seqlens_k, "cu_seqlens_k", dev, s + 1),
-            _ints(block_tables, "block_tables", dev, s, None), block_tables.shape[1], s, total, max_seqlen_q,
+            _table(block_tables, "block_tables", dev, s), block_tables.shape[1], s, total, max_seqlen_q,
             max_seqlen_k, hq, scale, _dense(out, "out", q.shape, dev), *_workspace_arg(workspace, dev))
     return out

@@ -11,7 +11,7 @@ import struct
 
 import torch
 
-from . import _cache_dims, _dense, _dev, _ints, _launch, _rows, _wrong
+from . import _dense, _ints, _launch, _rows, _wrong
 from .q4 import Q4Cache, _cache
 
 HEAD_DIM = 128
@@ -108,8 +108,10 @@ def qk_norm_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weig
     """qk_norm_rope, with its keys and v [N, Hkv, 128] written into the bf16 caches at slot_mapping; returns q_out."""
     qp, n, hq, qs = _rows(q, "q")
     dev = q.get_device()
-    _dev(k_cache, "k_cache", torch.bfloat16)
-    shape = nb, bs, hkv, d = _cache_dims(k_cache)
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        _wrong(k_cache, "k_cache", torch.bfloat16, dev, "[num_blocks, block_size, num_kv_heads, 128]")
+    shape = k_cache.shape
+    nb, bs, hkv, d = shape
     kp, _, _, ks = _rows(k, "k", dev, n, hkv)
     vp, _, _, vs = _rows(v, "v", dev, n, hkv)
     q_out, qo, qos = _like(q, q_out, "q_out", dev, n, hq)
