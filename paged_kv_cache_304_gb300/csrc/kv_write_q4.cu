@@ -39,7 +39,7 @@ __device__ __forceinline__ void store_chunk(const uint4& a, float inv, uint8_t* 
   for (int i = 0; i < 4; ++i) {
     y[2 * i] = q4::bf_lo(w[i]) * inv;
     y[2 * i + 1] = q4::bf_hi(w[i]) * inv;
-    m = q4::max_nan(m, q4::max_nan(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+    m = q4::max3_nan(m, fabsf(y[2 * i]), fabsf(y[2 * i + 1]));
   }
   m = q4::max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
   const uint32_t sb = q4::group_scale(m);

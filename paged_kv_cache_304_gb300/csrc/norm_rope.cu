@@ -50,9 +50,10 @@ __device__ __forceinline__ void store_q4(uint8_t* data, uint8_t* scales, int64_t
   float y[8], m = 0.f;
   unpack(a, y);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 8; i += 2) {
     y[i] *= inv;
-    m = q4::max_nan(m, fabsf(y[i]));
+    y[i + 1] *= inv;
+    m = q4::max3_nan(m, fabsf(y[i]), fabsf(y[i + 1]));
   }
   m = q4::max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
   const uint32_t sb = q4::group_scale(m);

@@ -80,8 +80,26 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Scale byte of a group whose largest |y| is `amax`.
-__device__ __forceinline__ uint32_t group_scale(float amax) { return enc_scale(__fdiv_rn(amax, 6.f)); }
+// Maximum of three that a NaN wins.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Scale byte of a group whose largest |y| is `amax`: e4m3(amax / 6), the quotient
+// correctly rounded (product with the reciprocal, corrected with its residual;
+// see enc8).  Everything from 2688 = 6 * 448 on saturates.
+__device__ __forceinline__ uint32_t group_scale(float amax) {
+  const float a = min_nan(amax, 4096.f), sixth = 1.f / 6.f;
+  const float q = a * sixth;
+  return enc_scale(fmaf(fmaf(-6.f, q, a), sixth, q));
+}
 
 // Eight codes of eight floats y over scale s (as the float its byte stands for);
 // `r` is 1 / s rounded to nearest.  A code depends on which side of a tie y / s
@@ -107,8 +125,9 @@ __device__ __forceinline__ uint32_t enc8_group(float* y, uint32_t sb, float amax
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(y[i], -FLT_MAX), FLT_MAX);
   }
-  const float s = dec_scale(sb);
-  return enc8(y, s, __frcp_rn(s));
+  // One Newton step on the approximate reciprocal (of four-bit numbers only).
+  const float s = dec_scale(sb), r = fast_rcp(s);
+  return enc8(y, s, fmaf(fmaf(-s, r, 1.f), r, r));
 }
 
 // bf16 pair word to two floats (exact).
