@@ -3,10 +3,10 @@ KV-cache write.
 
 Allowance: the output's rounding to bf16 is half a step, 2^-8 |y|.  The fp32
 part: the mean square over 128 dims and rsqrt are within 2^-20 relative, three
-products 2^-22, and the angle (its fraction of a turn rounded to fp32) within
-2 pi 2^-25 < 2^-22 rad plus sincospi's two units in the last place, 2^-22; a
-rotated value moves by at most that times the length of its pair: 2^-18 in all
-leaves room."""
+products 2^-22, and the angle (its fraction of a turn rounded to fp32, times
+2 pi) within 2 pi 2^-24 < 2^-21 rad plus the SFU's 2^-21 for a sine or cosine in
+[-pi, pi]; a rotated value moves by at most that times the length of its pair:
+2^-18 in all leaves room."""
 
 import numpy as np
 import pytest
