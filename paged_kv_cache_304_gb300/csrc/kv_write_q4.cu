@@ -33,17 +33,8 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
 // chunk `at` of the cache.
 __device__ __forceinline__ void store_chunk(const uint4& a, float inv, uint8_t* data, uint8_t* scales, int64_t at,
                                             int lane, bool real) {
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-  float y[8], m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    y[2 * i] = q4::bf_lo(w[i]) * inv;
-    y[2 * i + 1] = q4::bf_hi(w[i]) * inv;
-    m = q4::max3_nan(m, fabsf(y[2 * i]), fabsf(y[2 * i + 1]));
-  }
-  m = q4::max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  const uint32_t sb = q4::group_scale(m);
-  const uint32_t codes = q4::enc8_group(y, sb, m);
+  uint32_t sb;
+  const uint32_t codes = q4::quantise_chunk(a, inv, &sb);
   if (!real) return;
   *reinterpret_cast<uint32_t*>(data + at * 4) = codes;
   if (!(lane & 1)) scales[at >> 1] = static_cast<uint8_t>(sb);

@@ -12,13 +12,14 @@
 // in [-pi, pi], go to the SFU's sine and cosine (within 2^-21 there, a few
 // thousandths of the output's rounding).  No table of cosines is read.
 //
-// Bound by HBM (every row read and written once).  Eight lanes own a head, 16
-// dims each as two 8-dim chunks chosen so that both partners of a rotated pair
-// sit in one lane; a warp takes four heads at a time, the next four requested
-// while it works, and computes its lanes' eight sines and cosines once for all
-// heads of the token it handles.  With few tokens a token's heads are spread
-// over several warps.  fp32 arithmetic is done on pairs (one instruction for
-// two), which is what keeps the issue slots below the memory time.
+// Bound by HBM (every row read and written once).  A CTA takes a few tokens: it
+// puts their cosines and sines into shared memory, then its warps take units of
+// four heads of a token, eight lanes a head, 16 dims a lane as two 8-dim chunks
+// chosen so that both partners of a rotated pair sit in one lane.  Nothing is
+// carried from unit to unit, so the next unit's rows are requested while one is in
+// work and few registers leave room for many warps (with the angles and weights
+// kept in registers, 15 warps an SM reached 60 % of the copy bandwidth).  fp32
+// arithmetic is done on pairs (one instruction for two).
 #include <cuda_runtime.h>
 
 #include "pkv_device.cuh"
@@ -30,52 +31,38 @@ namespace {
 
 __device__ unsigned int g_err_norm_rope;
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
+constexpr int kMaxTokens = 8;          // of a CTA
+constexpr int kPairs = kHeadDim / 2;
 
-// Eight bf16 of a chunk as four pairs of floats, and back.
-__device__ __forceinline__ void unpack(const uint4& a, float2* x) {
-  x[0] = make_float2(q4::bf_lo(a.x), q4::bf_hi(a.x));
-  x[1] = make_float2(q4::bf_lo(a.y), q4::bf_hi(a.y));
-  x[2] = make_float2(q4::bf_lo(a.z), q4::bf_hi(a.z));
-  x[3] = make_float2(q4::bf_lo(a.w), q4::bf_hi(a.w));
-}
-
-__device__ __forceinline__ uint4 pack(const float2* x) {
+__device__ __forceinline__ uint4 pack8(const float2* x) {
   return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
                     pack_bf16x2(x[3].x, x[3].y));
 }
-
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
-// Quantise the lane's chunk (the other half of its group of 16 is in lane ^ 1)
-// and store it; `a` is the bf16 chunk.
-__device__ __forceinline__ void store_q4(uint8_t* data, uint8_t* scales, int64_t row, int chunk, const uint4& a,
-                                         float inv, bool write) {
-  float2 y2[4];
-  float y[8], m = 0.f;
-  unpack(a, y2);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    y2[i] = fmul2(y2[i], both(inv));
-    y[2 * i] = y2[i].x;
-    y[2 * i + 1] = y2[i].y;
-    m = q4::max3_nan(m, fabsf(y2[i].x), fabsf(y2[i].y));
-  }
-  m = q4::max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  const uint32_t sb = q4::group_scale(m);
-  const uint32_t w = q4::enc8_group(y, sb, m);
-  if (!write) return;
-  *reinterpret_cast<uint32_t*>(data + row * q4::kRowBytes + chunk * 4) = w;
-  if (!(chunk & 1)) scales[row * q4::kRowScales + (chunk >> 1)] = static_cast<uint8_t>(sb);
+// Eight floats from shared memory as four pairs.
+__device__ __forceinline__ void read8(const float* p, float2* x) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = make_float2(a.x, a.y);
+  x[1] = make_float2(a.z, a.w);
+  x[2] = make_float2(b.x, b.y);
+  x[3] = make_float2(b.z, b.w);
 }
 
 // kDest: 0 = k_out, 1 = bf16 cache (K and V), 2 = 4-bit cache (K and V).
 // kInter: rotated pairs are (2i, 2i + 1).
 template <int kDest, bool kInter>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormRopeArgs p, int splits) {
+__global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRopeArgs p, int tokens) {
+  __shared__ __align__(16) float s_cos[kMaxTokens][kPairs], s_sin[kMaxTokens][kPairs];
+  __shared__ __align__(16) float s_weight[2][kHeadDim];
+  __shared__ int s_slot[kMaxTokens];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  const int n = static_cast<int>(min(static_cast<int64_t>(tokens), p.num_tokens - t0));
+
   const int l = lane & 7, sub = lane >> 3;
   const int half_chunks = p.rope_dim >> 4;  // chunks in half of the rotated dims
   // The lane's chunks of 8 dims.  Rotated halves: chunk j and its partner
@@ -90,133 +77,147 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormRopeAr
       c1 = c0 + 8 - half_chunks;
     }
   }
-  // Groups of four heads: queries, then keys, then (with a cache) values.
+  // Units: groups of four heads (queries, then keys, then, with a cache, values)
+  // of the CTA's tokens.
   const int q_groups = (p.num_q_heads + 3) >> 2, kv_groups = (p.num_kv_heads + 3) >> 2;
   const int rope_groups = q_groups + kv_groups;
   const int groups = rope_groups + (kDest ? kv_groups : 0);
-  const int per = (groups + splits - 1) / splits;
-  const int64_t items = static_cast<int64_t>(p.num_tokens) * splits;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items; it += step) {
-    const int64_t t = it / splits;
-    const int g0 = static_cast<int>(it - t * splits) * per;
-    const int g1 = min(groups, g0 + per);
-    if (g0 >= g1) continue;
-    // Group g's row of this lane (plain loads: the output may be the input).
-    const uint16_t* q_row = p.q + t * p.q_stride;
-    const uint16_t* k_row = p.k + t * p.k_stride;
-    const uint16_t* v_row = p.v + t * p.v_stride;
-    auto load = [&](int g, uint4& a0, uint4& a1) {
-      const int head = 4 * (g < q_groups ? g : g < rope_groups ? g - q_groups : g - rope_groups) + sub;
-      const uint16_t* row = g < q_groups ? q_row : g < rope_groups ? k_row : v_row;
-      a0 = a1 = make_uint4(0u, 0u, 0u, 0u);
-      if (g < g1 && head < (g < q_groups ? p.num_q_heads : p.num_kv_heads)) {
-        const uint4* src = reinterpret_cast<const uint4*>(row + head * kHeadDim);
-        a0 = src[c0];
-        a1 = src[c1];
+  // Rows of unit (t, g), this lane's head of the four (plain loads: the output may be the input).
+  auto load = [&](int t, int g, uint4& a0, uint4& a1) {
+    a0 = a1 = make_uint4(0u, 0u, 0u, 0u);
+    if (t >= n) return;
+    const bool is_q = g < q_groups;
+    const int head = 4 * (is_q ? g : g < rope_groups ? g - q_groups : g - rope_groups) + sub;
+    if (head >= (is_q ? p.num_q_heads : p.num_kv_heads)) return;
+    const uint16_t* row = is_q ? p.q + (t0 + t) * p.q_stride
+                               : g < rope_groups ? p.k + (t0 + t) * p.k_stride : p.v + (t0 + t) * p.v_stride;
+    const uint4* src = reinterpret_cast<const uint4*>(row + head * kHeadDim);
+    a0 = src[c0];
+    a1 = src[c1];
+  };
+  int t = warp / groups, g = warp - t * groups;
+  uint4 n0, n1;
+  load(t, g, n0, n1);
+
+  // Cosines and sines of every token (pairs behind rope_dim do not turn), weights, slots.
+  for (int i = threadIdx.x; i < n * kPairs; i += 32 * kWarps) {
+    const int pair = i % kPairs, tok = i / kPairs;
+    float c = 1.f, s = 0.f;
+    if (2 * pair < p.rope_dim) {
+      const int axis = pair < p.section_end0 ? 0 : (pair < p.section_end1 ? 1 : 2);
+      const int pos = __ldg(p.positions + axis * p.position_axis_stride + t0 + tok);
+      const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(pos)) *
+                            static_cast<uint64_t>(__ldg(reinterpret_cast<const long long*>(p.freqs) + pair));
+      // angle in [-pi, pi): the top 32 bits times 2 pi / 2^32
+      const float angle = static_cast<float>(static_cast<int>(frac >> 32)) * 1.4629180792671596e-9f;
+      c = __cosf(angle);
+      s = __sinf(angle);
+    }
+    s_cos[tok][pair] = c;
+    s_sin[tok][pair] = s;
+  }
+  {
+    const uint16_t* w = threadIdx.x < kHeadDim ? p.q_weight : p.k_weight;
+    const int d = threadIdx.x % kHeadDim;
+    s_weight[threadIdx.x / kHeadDim][d] = w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + d)) << 16) : 1.f;
+  }
+  if (kDest && threadIdx.x < n) {
+    int s = __ldg(p.slots + t0 + threadIdx.x);
+    if (s < -1 || s >= p.num_blocks * kBlockSize) {
+      atomicOr(&g_err_norm_rope, PKV_DEVERR_SLOT_RANGE);
+      s = -1;
+    }
+    s_slot[threadIdx.x] = s;
+  }
+  __syncthreads();
+
+  while (t < n) {
+    uint4 a0 = n0, a1 = n1;
+    int tn = t, gn = g + kWarps;
+    while (gn >= groups) {
+      gn -= groups;
+      ++tn;
+    }
+    load(tn, gn, n0, n1);
+    const bool is_q = g < q_groups, is_v = g >= rope_groups;
+    const int head = 4 * (is_q ? g : is_v ? g - rope_groups : g - q_groups) + sub;
+    const bool real = head < (is_q ? p.num_q_heads : p.num_kv_heads);
+    if (!is_v) {
+      float2 x[8], w[8];
+      q4::unpack8(a0, x);
+      q4::unpack8(a1, x + 4);
+      if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
+        float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = ffma2(x[i], x[i], ss);
+        float sum = ss.x + ss.y;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        const float r = rsqrtf(sum * (1.f / kHeadDim) + p.eps);
+        read8(s_weight[is_q ? 0 : 1] + 8 * c0, w);
+        read8(s_weight[is_q ? 0 : 1] + 8 * c1, w + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fmul2(fmul2(x[i], both(r)), w[i]);
       }
-    };
-    uint4 n0, n1;
-    load(g0, n0, n1);
-    int64_t slot = -1;
-    if (kDest) {
-      slot = __ldg(p.slots + t);
-      if (slot < -1 || slot >= static_cast<int64_t>(p.num_blocks) * kBlockSize) {
-        if (lane == 0) atomicOr(&g_err_norm_rope, PKV_DEVERR_SLOT_RANGE);
-        slot = -1;
+      // The lane's pairs: elements of chunk c0 with those of c1 (halves), or
+      // neighbours within each chunk (interleaved).
+      float2 c[4], s[4];
+      if (kInter) {
+        const float4 ca = *reinterpret_cast<const float4*>(&s_cos[t][4 * c0]);
+        const float4 cb = *reinterpret_cast<const float4*>(&s_cos[t][4 * c1]);
+        const float4 sa = *reinterpret_cast<const float4*>(&s_sin[t][4 * c0]);
+        const float4 sb = *reinterpret_cast<const float4*>(&s_sin[t][4 * c1]);
+        const float ce[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+        const float se[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[e] = ffma2(make_float2(x[e].y, x[e].x), make_float2(-se[e], se[e]), fmul2(x[e], both(ce[e])));
+      } else {
+        read8(&s_cos[t][8 * l], c);
+        read8(&s_sin[t][8 * l], s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 u = x[e], z = x[e + 4];
+          x[e] = ffma2(z, make_float2(-s[e].x, -s[e].y), fmul2(u, c[e]));
+          x[e + 4] = ffma2(u, s[e], fmul2(z, c[e]));
+        }
+      }
+      a0 = pack8(x);
+      a1 = pack8(x + 4);
+    }
+    const int64_t slot = kDest ? s_slot[t] : 0;
+    if (is_q || kDest < 2) {
+      uint16_t* o = nullptr;
+      if (is_q)
+        o = p.q_out + (t0 + t) * p.q_out_stride;
+      else if (kDest == 0)
+        o = p.k_out + (t0 + t) * p.k_out_stride;
+      else if (slot >= 0)
+        o = (is_v ? p.v_cache : p.k_cache) + slot * p.num_kv_heads * kHeadDim;
+      if (real && o) {
+        uint4* dst = reinterpret_cast<uint4*>(o + head * kHeadDim);
+        dst[c0] = a0;
+        dst[c1] = a1;
+      }
+    } else if (slot >= 0) {  // the whole warp
+      const int64_t row = slot * p.num_kv_heads + head;
+      const float inv = is_v ? p.q4.v_inv : p.q4.k_inv;
+      uint32_t b0, b1;
+      const uint32_t w0 = q4::quantise_chunk(a0, inv, &b0), w1 = q4::quantise_chunk(a1, inv, &b1);
+      if (real) {
+        uint32_t* data = reinterpret_cast<uint32_t*>((is_v ? p.q4.v_data : p.q4.k_data) + row * q4::kRowBytes);
+        uint8_t* scales = (is_v ? p.q4.v_scales : p.q4.k_scales) + row * q4::kRowScales;
+        data[c0] = w0;
+        data[c1] = w1;
+        if (!(lane & 1)) {  // even chunks: the scale of a group of two
+          scales[c0 >> 1] = static_cast<uint8_t>(b0);
+          scales[c1 >> 1] = static_cast<uint8_t>(b1);
+        }
       }
     }
-    // Cosines and sines of the lane's pairs: elements (2e, 2e + 1) of chunk c0
-    // with those of c1 (halves), or pair e of the lane's chunks (interleaved).
-    float cs[8], sn[8];
-    if (g0 < rope_groups) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = kInter ? (e < 4 ? 4 * c0 + e : 4 * c1 + e - 4) : 8 * l + e;
-        cs[e] = 1.f;
-        sn[e] = 0.f;
-        if (kInter ? 2 * i < p.rope_dim : l < half_chunks) {
-          const int axis = i < p.section_end0 ? 0 : (i < p.section_end1 ? 1 : 2);
-          const int pos = __ldg(p.positions + axis * p.position_axis_stride + t);
-          const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(pos)) *
-                                static_cast<uint64_t>(__ldg(reinterpret_cast<const long long*>(p.freqs) + i));
-          // angle in [-pi, pi): the top 32 bits times 2 pi / 2^32
-          const float angle = static_cast<float>(static_cast<int>(frac >> 32)) * 1.4629180792671596e-9f;
-          cs[e] = __cosf(angle);
-          sn[e] = __sinf(angle);
-        }
-      }
-    }
-    float2 w[8];       // weights of the lane's 16 dims, of the phase's kind of row
-    bool norm = false;
-    for (int g = g0; g < g1; ++g) {
-      uint4 a0 = n0, a1 = n1;
-      load(g + 1, n0, n1);
-      const bool is_q = g < q_groups, is_v = g >= rope_groups;
-      const int head = 4 * (is_q ? g : is_v ? g - rope_groups : g - q_groups) + sub;
-      const bool real = head < (is_q ? p.num_q_heads : p.num_kv_heads);
-      if (!is_v) {
-        if (g == g0 || g == q_groups) {
-          const uint4* src = reinterpret_cast<const uint4*>(is_q ? p.q_weight : p.k_weight);
-          norm = src != nullptr;
-          if (norm) {
-            unpack(__ldg(src + c0), w);
-            unpack(__ldg(src + c1), w + 4);
-          }
-        }
-        float2 x[8];
-        unpack(a0, x);
-        unpack(a1, x + 4);
-        if (norm) {
-          float2 ss = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = ffma2(x[i], x[i], ss);
-          float sum = ss.x + ss.y;
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-          const float r = rsqrtf(sum * (1.f / kHeadDim) + p.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = fmul2(fmul2(x[i], both(r)), w[i]);
-        }
-        if (kInter) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            x[e] = ffma2(make_float2(x[e].y, x[e].x), make_float2(-sn[e], sn[e]), fmul2(x[e], both(cs[e])));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 c = make_float2(cs[2 * e], cs[2 * e + 1]), s = make_float2(sn[2 * e], sn[2 * e + 1]);
-            const float2 u = x[e], z = x[e + 4];
-            x[e] = ffma2(z, make_float2(-s.x, -s.y), fmul2(u, c));
-            x[e + 4] = ffma2(u, s, fmul2(z, c));
-          }
-        }
-        a0 = pack(x);
-        a1 = pack(x + 4);
-      }
-      if (is_q || kDest == 0) {
-        if (real) {
-          uint4* o = reinterpret_cast<uint4*>((is_q ? p.q_out + t * p.q_out_stride : p.k_out + t * p.k_out_stride) +
-                                              head * kHeadDim);
-          o[c0] = a0;
-          o[c1] = a1;
-        }
-      } else if (kDest == 1) {
-        if (real && slot >= 0) {
-          uint4* o = reinterpret_cast<uint4*>((is_v ? p.v_cache : p.k_cache) + (slot * p.num_kv_heads + head) * kHeadDim);
-          o[c0] = a0;
-          o[c1] = a1;
-        }
-      } else if (slot >= 0) {  // the whole warp
-        const int64_t row = slot * p.num_kv_heads + head;
-        uint8_t* data = is_v ? p.q4.v_data : p.q4.k_data;
-        uint8_t* scales = is_v ? p.q4.v_scales : p.q4.k_scales;
-        const float inv = is_v ? p.q4.v_inv : p.q4.k_inv;
-        store_q4(data, scales, row, c0, a0, inv, real);
-        store_q4(data, scales, row, c1, a1, inv, real);
-      }
-    }
+    t = tn;
+    g = gn;
   }
 }
 
@@ -224,20 +225,17 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormRopeAr
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int dest, int num_sms, cudaStream_t stream) {
   if (a.num_tokens == 0) return cudaSuccess;
-  const int kv_groups = (a.num_kv_heads + 3) / 4;
-  const int groups = (a.num_q_heads + 3) / 4 + kv_groups * (dest ? 2 : 1);
-  // Few tokens: spread a token's heads over warps until the GPU has ~8 warps an SM.
-  int splits = 1;
-  while (splits < groups && static_cast<int64_t>(a.num_tokens) * splits < static_cast<int64_t>(num_sms) * 8) ++splits;
-  const int64_t items = static_cast<int64_t>(a.num_tokens) * splits;
-  const int64_t blocks = std::min<int64_t>((items + kWarps - 1) / kWarps, static_cast<int64_t>(num_sms) * 32);
-  const dim3 grid(static_cast<unsigned>(blocks)), block(32 * kWarps);
+  // Up to eight tokens a CTA (their angles are computed once), fewer while that
+  // would leave SMs without two CTAs.
+  const int tokens =
+      static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxTokens, a.num_tokens / (2 * static_cast<int64_t>(num_sms)))));
+  const dim3 grid(static_cast<unsigned>((a.num_tokens + tokens - 1) / tokens)), block(32 * kWarps);
   void (*kernel)(NormRopeArgs, int) = nullptr;
   if (a.interleaved)
     kernel = dest == 0 ? norm_rope_kernel<0, true> : dest == 1 ? norm_rope_kernel<1, true> : norm_rope_kernel<2, true>;
   else
     kernel = dest == 0 ? norm_rope_kernel<0, false> : dest == 1 ? norm_rope_kernel<1, false> : norm_rope_kernel<2, false>;
-  return launch_pdl(kernel, grid, block, 0, stream, a, splits);
+  return launch_pdl(kernel, grid, block, 0, stream, a, tokens);
 }
 
 PKV_DEFINE_READ_ERROR(read_error_norm_rope, g_err_norm_rope)

@@ -27,15 +27,6 @@ constexpr int kGroup = 16;       // dims that share a scale
 constexpr int kRowBytes = 64;    // codes of one head's row
 constexpr int kRowScales = 8;    // scales of one head's row
 
-// Two codes from two floats: `lo` in bits 0-3.
-__device__ __forceinline__ uint32_t enc2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
-      : "=r"(r)
-      : "f"(hi), "f"(lo));
-  return r;
-}
-
 // The four bytes of a word as four fp16 pairs: out[i] = codes 2i (low half), 2i+1.
 __device__ __forceinline__ void dec8(uint32_t w, uint32_t (&out)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
@@ -101,29 +92,38 @@ __device__ __forceinline__ uint32_t group_scale(float amax) {
   return enc_scale(fmaf(fmaf(-6.f, q, a), sixth, q));
 }
 
-// Eight codes of eight floats y over scale s (as the float its byte stands for);
-// `r` is 1 / s rounded to nearest.  A code depends on which side of a tie y / s
-// lies, so the quotient is needed correctly rounded (a tie is representable, and
-// a quotient that is none does not round to one): the product y r is corrected
-// with its residual, q + (y - q s) r (Markstein, "Computation of elementary
-// functions on the IBM RISC System/6000 processor", 1990).  An infinite y is
-// taken as its largest code before.
-__device__ __forceinline__ uint32_t enc8(const float* y, float s, float r) {
-  uint32_t w = 0;
-  if (s == 0.f) return 0u;
+// Eight codes of four pairs of floats y over scale s (as the float its byte stands
+// for); `r` is 1 / s rounded to nearest.  A code depends on which side of a tie
+// y / s lies, so the quotient is needed correctly rounded (a tie is
+// representable, and a quotient that is none does not round to one): the product
+// y r is corrected with its residual, q + (y - q s) r (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990).
+__device__ __forceinline__ uint32_t enc8(const float2* y, float s, float r) {
+  const float2 r2 = make_float2(r, r), ns = make_float2(-s, -s);
+  float2 q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = y[2 * i] * r, b = y[2 * i + 1] * r;
-    w |= enc2(fmaf(fmaf(-a, s, y[2 * i]), r, a), fmaf(fmaf(-b, s, y[2 * i + 1]), r, b)) << (8 * i);
+    const float2 a = fmul2(y[i], r2);
+    q[i] = ffma2(ffma2(a, ns, y[i]), r2, a);
   }
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(q[0].x), "f"(q[0].y), "f"(q[1].x), "f"(q[1].y), "f"(q[2].x), "f"(q[2].y), "f"(q[3].x), "f"(q[3].y));
   return w;
 }
 
-// Codes of eight floats whose group's scale byte is `sb`.
-__device__ __forceinline__ uint32_t enc8_group(float* y, uint32_t sb, float amax) {
+// Codes of eight floats of a group with largest magnitude `amax` and scale byte
+// `sb`.  An infinite y is taken as the largest number, a group of scale zero gets
+// codes 0.
+__device__ __forceinline__ uint32_t enc8_group(float2* y, uint32_t sb, float amax) {
+  if (sb == 0) return 0u;
   if (amax == INFINITY) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(y[i], -FLT_MAX), FLT_MAX);
+    for (int i = 0; i < 4; ++i)
+      y[i] = make_float2(fminf(fmaxf(y[i].x, -FLT_MAX), FLT_MAX), fminf(fmaxf(y[i].y, -FLT_MAX), FLT_MAX));
   }
   // One Newton step on the approximate reciprocal (of four-bit numbers only).
   const float s = dec_scale(sb), r = fast_rcp(s);
@@ -133,6 +133,30 @@ __device__ __forceinline__ uint32_t enc8_group(float* y, uint32_t sb, float amax
 // bf16 pair word to two floats (exact).
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Eight bf16 as four pairs of floats.
+__device__ __forceinline__ void unpack8(const uint4& a, float2* x) {
+  x[0] = make_float2(bf_lo(a.x), bf_hi(a.x));
+  x[1] = make_float2(bf_lo(a.y), bf_hi(a.y));
+  x[2] = make_float2(bf_lo(a.z), bf_hi(a.z));
+  x[3] = make_float2(bf_lo(a.w), bf_hi(a.w));
+}
+
+// Quantise a chunk of eight bf16 whose group's other half is in lane ^ 1 (the
+// whole warp takes part): the codes, and in *sb the group's scale byte.
+__device__ __forceinline__ uint32_t quantise_chunk(const uint4& a, float inv, uint32_t* sb) {
+  float2 y[4];
+  unpack8(a, y);
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[i] = fmul2(y[i], make_float2(inv, inv));
+    m = max3_nan(m, fabsf(y[i].x), fabsf(y[i].y));
+  }
+  m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  *sb = group_scale(m);
+  return enc8_group(y, *sb, m);
+}
 
 }  // namespace q4
 }  // namespace pkv
