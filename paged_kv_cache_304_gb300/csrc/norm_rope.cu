@@ -15,11 +15,13 @@
 // Bound by HBM (every row read and written once).  A CTA takes a few tokens: it
 // puts their cosines and sines into shared memory, then its warps take units of
 // four heads of a token, eight lanes a head, 16 dims a lane as two 8-dim chunks
-// chosen so that both partners of a rotated pair sit in one lane.  Nothing is
+// chosen so that both partners of a rotated pair sit in one lane.  Little is
 // carried from unit to unit, so the next unit's rows are requested while one is in
 // work and few registers leave room for many warps (with the angles and weights
-// kept in registers, 15 warps an SM reached 60 % of the copy bandwidth).  fp32
-// arithmetic is done on pairs (one instruction for two).
+// kept in registers, 15 warps an SM reached 60 % of the copy bandwidth).  Issue
+// slots are the second limit: fp32 arithmetic is done on pairs (one instruction
+// for two), and a warp takes one group of heads through all of the CTA's tokens,
+// so that 64-bit addresses are only stepped.
 #include <cuda_runtime.h>
 
 #include "pkv_device.cuh"
@@ -32,8 +34,9 @@ namespace {
 __device__ unsigned int g_err_norm_rope;
 
 constexpr int kWarps = 8;
-constexpr int kMaxTokens = 8;          // of a CTA
+constexpr int kMaxTokens = 16;         // of a CTA
 constexpr int kPairs = kHeadDim / 2;
+constexpr int kChunks = kHeadDim / 8;  // 16-byte chunks of a row
 
 __device__ __forceinline__ uint4 pack8(const float2* x) {
   return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
@@ -41,13 +44,15 @@ __device__ __forceinline__ uint4 pack8(const float2* x) {
 }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
-// Eight floats from shared memory as four pairs.
-__device__ __forceinline__ void read8(const float* p, float2* x) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+// Four, eight floats from shared memory as pairs.
+__device__ __forceinline__ void read4(const float* p, float2* x) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
   x[0] = make_float2(a.x, a.y);
   x[1] = make_float2(a.z, a.w);
-  x[2] = make_float2(b.x, b.y);
-  x[3] = make_float2(b.z, b.w);
+}
+__device__ __forceinline__ void read8(const float* p, float2* x) {
+  read4(p, x);
+  read4(p + 4, x + 2);
 }
 
 // kDest: 0 = k_out, 1 = bf16 cache (K and V), 2 = 4-bit cache (K and V).
@@ -82,23 +87,6 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
   const int q_groups = (p.num_q_heads + 3) >> 2, kv_groups = (p.num_kv_heads + 3) >> 2;
   const int rope_groups = q_groups + kv_groups;
   const int groups = rope_groups + (kDest ? kv_groups : 0);
-  // Rows of unit (t, g), this lane's head of the four (plain loads: the output may be the input).
-  auto load = [&](int t, int g, uint4& a0, uint4& a1) {
-    a0 = a1 = make_uint4(0u, 0u, 0u, 0u);
-    if (t >= n) return;
-    const bool is_q = g < q_groups;
-    const int head = 4 * (is_q ? g : g < rope_groups ? g - q_groups : g - rope_groups) + sub;
-    if (head >= (is_q ? p.num_q_heads : p.num_kv_heads)) return;
-    const uint16_t* row = is_q ? p.q + (t0 + t) * p.q_stride
-                               : g < rope_groups ? p.k + (t0 + t) * p.k_stride : p.v + (t0 + t) * p.v_stride;
-    const uint4* src = reinterpret_cast<const uint4*>(row + head * kHeadDim);
-    a0 = src[c0];
-    a1 = src[c1];
-  };
-  int t = warp / groups, g = warp - t * groups;
-  uint4 n0, n1;
-  load(t, g, n0, n1);
-
   // Cosines and sines of every token (pairs behind rope_dim do not turn), weights, slots.
   for (int i = threadIdx.x; i < n * kPairs; i += 32 * kWarps) {
     const int pair = i % kPairs, tok = i / kPairs;
@@ -131,93 +119,120 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
   }
   __syncthreads();
 
-  while (t < n) {
-    uint4 a0 = n0, a1 = n1;
-    int tn = t, gn = g + kWarps;
-    while (gn >= groups) {
-      gn -= groups;
-      ++tn;
-    }
-    load(tn, gn, n0, n1);
+  // A warp's run of units, all tokens of one group before the next group.
+  const int units = groups * n;
+  int u = units * warp / kWarps;
+  const int u_end = units * (warp + 1) / kWarps;
+  while (u < u_end) {
+    const int g = u / n, t_begin = u - g * n;
+    const int t_end = min(n, t_begin + u_end - u);
+    u += t_end - t_begin;
     const bool is_q = g < q_groups, is_v = g >= rope_groups;
     const int head = 4 * (is_q ? g : is_v ? g - rope_groups : g - q_groups) + sub;
     const bool real = head < (is_q ? p.num_q_heads : p.num_kv_heads);
-    if (!is_v) {
-      float2 x[8], w[8];
-      q4::unpack8(a0, x);
-      q4::unpack8(a1, x + 4);
-      if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
-        float2 ss = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = ffma2(x[i], x[i], ss);
-        float sum = ss.x + ss.y;
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        const float r = rsqrtf(sum * (1.f / kHeadDim) + p.eps);
-        read8(s_weight[is_q ? 0 : 1] + 8 * c0, w);
-        read8(s_weight[is_q ? 0 : 1] + 8 * c1, w + 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fmul2(fmul2(x[i], both(r)), w[i]);
+    // Steps and places in 16-byte chunks; plain loads: the output may be the input.
+    const int64_t step = (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) >> 3;
+    const uint4* src = reinterpret_cast<const uint4*>(is_q ? p.q : is_v ? p.v : p.k) + (t0 + t_begin) * step + head * kChunks;
+    const int64_t out_step = (is_q ? p.q_out_stride : p.k_out_stride) >> 3;
+    uint4* out = reinterpret_cast<uint4*>(is_q ? p.q_out : p.k_out) + (t0 + t_begin) * out_step + head * kChunks;
+    const bool norm = (is_q ? p.q_weight : p.k_weight) != nullptr;
+    const float* weight = s_weight[is_q ? 0 : 1];
+    const bool to_cache = kDest != 0 && !is_q;
+    // row 0 of this lane's head in the cache (kDest 1: 16-byte chunks; 2: bytes)
+    uint4* rows16 = reinterpret_cast<uint4*>(is_v ? p.v_cache : p.k_cache) + head * kChunks;
+    uint8_t* data = (is_v ? p.q4.v_data : p.q4.k_data) + head * q4::kRowBytes;
+    uint8_t* scales = (is_v ? p.q4.v_scales : p.q4.k_scales) + head * q4::kRowScales;
+    const float inv = is_v ? p.q4.v_inv : p.q4.k_inv;
+    uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
+    if (real) {
+      n0 = src[c0];
+      n1 = src[c1];
+    }
+    for (int t = t_begin; t < t_end; ++t) {
+      uint4 a0 = n0, a1 = n1;
+      src += step;
+      if (real && t + 1 < t_end) {
+        n0 = src[c0];
+        n1 = src[c1];
       }
-      // The lane's pairs: elements of chunk c0 with those of c1 (halves), or
-      // neighbours within each chunk (interleaved).
-      float2 c[4], s[4];
-      if (kInter) {
-        const float4 ca = *reinterpret_cast<const float4*>(&s_cos[t][4 * c0]);
-        const float4 cb = *reinterpret_cast<const float4*>(&s_cos[t][4 * c1]);
-        const float4 sa = *reinterpret_cast<const float4*>(&s_sin[t][4 * c0]);
-        const float4 sb = *reinterpret_cast<const float4*>(&s_sin[t][4 * c1]);
-        const float ce[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
-        const float se[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+      if (!is_v) {
+        float2 x[8];
+        q4::unpack8(a0, x);
+        q4::unpack8(a1, x + 4);
+        if (norm) {
+          float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          x[e] = ffma2(make_float2(x[e].y, x[e].x), make_float2(-se[e], se[e]), fmul2(x[e], both(ce[e])));
-      } else {
-        read8(&s_cos[t][8 * l], c);
-        read8(&s_sin[t][8 * l], s);
+          for (int i = 0; i < 8; ++i) ss = ffma2(x[i], x[i], ss);
+          float sum = ss.x + ss.y;
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+          const float2 r = both(rsqrtf(sum * (1.f / kHeadDim) + p.eps));
+          float2 w[4];
+          read8(weight + 8 * c0, w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 u = x[e], z = x[e + 4];
-          x[e] = ffma2(z, make_float2(-s[e].x, -s[e].y), fmul2(u, c[e]));
-          x[e + 4] = ffma2(u, s[e], fmul2(z, c[e]));
+          for (int i = 0; i < 4; ++i) x[i] = fmul2(fmul2(x[i], r), w[i]);
+          read8(weight + 8 * c1, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i + 4] = fmul2(fmul2(x[i + 4], r), w[i]);
+        }
+        // The lane's pairs: elements of chunk c0 with those of c1 (halves), or
+        // neighbours within each chunk (interleaved: pairs 4 c0 .., 4 c1 ..).
+        float2 c[4], s[4];
+        if (kInter) {
+          read4(&s_cos[t][4 * c0], c);
+          read4(&s_cos[t][4 * c1], c + 2);
+          read4(&s_sin[t][4 * c0], s);
+          read4(&s_sin[t][4 * c1], s + 2);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float ce = e & 1 ? c[e >> 1].y : c[e >> 1].x, se = e & 1 ? s[e >> 1].y : s[e >> 1].x;
+            const float2 z = x[e];
+            x[e] = make_float2(fmaf(-z.y, se, z.x * ce), fmaf(z.x, se, z.y * ce));
+          }
+        } else {
+          read8(&s_cos[t][8 * l], c);
+          read8(&s_sin[t][8 * l], s);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = x[e], z = x[e + 4];
+            x[e] = ffma2(z, make_float2(-s[e].x, -s[e].y), fmul2(v, c[e]));
+            x[e + 4] = ffma2(v, s[e], fmul2(z, c[e]));
+          }
+        }
+        a0 = pack8(x);
+        a1 = pack8(x + 4);
+      }
+      if (!to_cache) {
+        if (real) {
+          out[c0] = a0;
+          out[c1] = a1;
+        }
+        out += out_step;
+      } else if (const int slot = s_slot[t]; slot >= 0) {  // the whole warp
+        const int64_t row = static_cast<int64_t>(slot) * p.num_kv_heads;
+        if (kDest == 1) {
+          if (real) {
+            uint4* dst = rows16 + row * kChunks;
+            dst[c0] = a0;
+            dst[c1] = a1;
+          }
+        } else {
+          uint32_t b0, b1;
+          const uint32_t w0 = q4::quantise_chunk(a0, inv, &b0), w1 = q4::quantise_chunk(a1, inv, &b1);
+          if (real) {
+            uint32_t* d = reinterpret_cast<uint32_t*>(data + row * q4::kRowBytes);
+            d[c0] = w0;
+            d[c1] = w1;
+            if (!(lane & 1)) {  // even chunks: the scale of a group of two
+              uint8_t* sc = scales + row * q4::kRowScales;
+              sc[c0 >> 1] = static_cast<uint8_t>(b0);
+              sc[c1 >> 1] = static_cast<uint8_t>(b1);
+            }
+          }
         }
       }
-      a0 = pack8(x);
-      a1 = pack8(x + 4);
     }
-    const int64_t slot = kDest ? s_slot[t] : 0;
-    if (is_q || kDest < 2) {
-      uint16_t* o = nullptr;
-      if (is_q)
-        o = p.q_out + (t0 + t) * p.q_out_stride;
-      else if (kDest == 0)
-        o = p.k_out + (t0 + t) * p.k_out_stride;
-      else if (slot >= 0)
-        o = (is_v ? p.v_cache : p.k_cache) + slot * p.num_kv_heads * kHeadDim;
-      if (real && o) {
-        uint4* dst = reinterpret_cast<uint4*>(o + head * kHeadDim);
-        dst[c0] = a0;
-        dst[c1] = a1;
-      }
-    } else if (slot >= 0) {  // the whole warp
-      const int64_t row = slot * p.num_kv_heads + head;
-      const float inv = is_v ? p.q4.v_inv : p.q4.k_inv;
-      uint32_t b0, b1;
-      const uint32_t w0 = q4::quantise_chunk(a0, inv, &b0), w1 = q4::quantise_chunk(a1, inv, &b1);
-      if (real) {
-        uint32_t* data = reinterpret_cast<uint32_t*>((is_v ? p.q4.v_data : p.q4.k_data) + row * q4::kRowBytes);
-        uint8_t* scales = (is_v ? p.q4.v_scales : p.q4.k_scales) + row * q4::kRowScales;
-        data[c0] = w0;
-        data[c1] = w1;
-        if (!(lane & 1)) {  // even chunks: the scale of a group of two
-          scales[c0 >> 1] = static_cast<uint8_t>(b0);
-          scales[c1 >> 1] = static_cast<uint8_t>(b1);
-        }
-      }
-    }
-    t = tn;
-    g = gn;
   }
 }
 
@@ -225,10 +240,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int dest, int num_sms, cudaStream_t stream) {
   if (a.num_tokens == 0) return cudaSuccess;
-  // Up to eight tokens a CTA (their angles are computed once), fewer while that
-  // would leave SMs without two CTAs.
-  const int tokens =
-      static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxTokens, a.num_tokens / (2 * static_cast<int64_t>(num_sms)))));
+  // At most sixteen tokens a CTA, as many as fill whole waves of four CTAs an SM.
+  const int64_t wave = 4 * static_cast<int64_t>(num_sms);
+  const int64_t waves = (a.num_tokens + kMaxTokens * wave - 1) / (kMaxTokens * wave);
+  const int tokens = static_cast<int>((a.num_tokens + wave * waves - 1) / (wave * waves));
   const dim3 grid(static_cast<unsigned>((a.num_tokens + tokens - 1) / tokens)), block(32 * kWarps);
   void (*kernel)(NormRopeArgs, int) = nullptr;
   if (a.interleaved)
