@@ -15,8 +15,10 @@
 //   place, thread r its row r, scaled by a power of two so that the row's largest
 //   element is in [2^14, 2^15); then the softmax, thread r on row r (TMEM lane
 //   r), with the power of two undone in the row's softmax scale.
-// * warps 12-15: thread i turns token i of the 128-token K and V tiles into fp16:
-//   64 bytes of codes and 8 scales, fetched a tile ahead into registers, become
+// * warps 12-15 (with one slot only, warps 8-11 take the V tiles): thread i turns token i of the 128-token K and V tiles into fp16:
+//   64 bytes of codes and 8 scales, fetched into registers one step ahead (with one
+//   slot, where the loads' latency shows, also prefetched into L2 six steps ahead;
+//   with two, whose K/V tiles other CTAs read as well, that cost 14 %), become
 //   128 dims (one conversion and one multiplication per two dims, exact) written
 //   in the 128-byte swizzle that the matrix descriptors expect.
 // Tensor memory: S (128 columns, handed from slot to slot), P_A | P_B (64 each,
@@ -26,8 +28,11 @@
 // it: their scores are masked and their V rows written as zeros.  A V group that
 // holds a NaN is written as zeros as well and the NaN goes into its token's K row
 // instead, so that it reaches the queries that see the token and no others.
-// With too few tiles for the GPU the keys are split over several CTAs, which
-// leave (max, sum, unnormalised output) triples for a combine kernel.
+// With too few query tiles for the GPU ("split mode") the grid is one CTA per SM
+// and the keys are split: every CTA finds the smallest number C of K/V tiles for
+// which ceil(tiles / C) pieces of every query tile need no more CTAs than there
+// are, and takes its piece.  Pieces leave (max, sum, unnormalised output) triples
+// for a combine kernel.
 // Every wait is bounded (two seconds); on timeout the CTA flags
 // PKV_DEVERR_WAIT_TIMEOUT, lets the copies and MMAs it has already issued
 // complete, frees its tensor memory and returns.
@@ -65,9 +70,11 @@ struct Params {
   const int32_t* tables;
   uint16_t* out;
   Q4Cache c;
-  float* ws_o;    // [split, token, head, 128], only with several splits
-  float2* ws_ml;  // [split, token, head] (row max in log2 units, row sum)
-  int32_t maxb, Hq, Hkv, G, groups, npairs, total_q, max_q, max_k, splits;
+  float* ws_o;    // [piece, token, head, 128], only in split mode
+  float2* ws_ml;  // [piece, token, head] (row max in log2 units, row sum)
+  int32_t* ws_pieces;  // [sequence, tile rank] pieces of a query tile
+  int32_t maxb, S, Hq, Hkv, G, groups, npairs, tiles, total_q, max_q, max_k;
+  int32_t pieces;      // 0: no split; else the most pieces that a query tile may have
   int32_t log2_heads;  // heads of a slot: 2^log2_heads
   float sl2;           // scale * k_scale * log2(e)
 };
@@ -162,6 +169,15 @@ struct Packed {
 // Bytes of w that are e4m3 NaNs, as 0xff.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
+// L2 prefetch of token `i`'s row of 128-token tile j (its codes and scales).
+__device__ __forceinline__ void prefetch_row(const Params& p, const int32_t* table, int j, bool is_v, int i, int g) {
+  const int phys = __ldg(table + (j >> 1));
+  if (phys < 0 || phys >= p.c.num_blocks) return;
+  const int64_t row = (static_cast<int64_t>(phys) * kBlockSize + (j & 1) * kTileN + i) * p.Hkv + g;
+  asm volatile("prefetch.global.L2 [%0];" ::"l"((is_v ? p.c.v_data : p.c.k_data) + row * q4::kRowBytes));
+  asm volatile("prefetch.global.L2 [%0];" ::"l"((is_v ? p.c.v_scales : p.c.k_scales) + row * q4::kRowScales));
+}
+
 // Token `i` of 128-token tile j of K or V, kv head g.
 __device__ __forceinline__ void fetch(const Params& p, const int32_t* table, int j, bool is_v, int i, int g, int len,
                                       Packed& o) {
@@ -209,34 +225,187 @@ __device__ __forceinline__ void expand(const Packed& x, uint32_t dst, int i) {
   }
 }
 
+// A sequence of the call.
+struct Seq {
+  int q0, n, len;  // first row, new tokens, keys
+  bool ok;
+};
+__device__ __forceinline__ Seq load_seq(const Params& p, int seq) {
+  Seq s;
+  s.q0 = __ldg(p.cu_q + seq);
+  const int q1 = __ldg(p.cu_q + seq + 1);
+  s.n = q1 - s.q0;
+  s.len = __ldg(p.cu_k + seq + 1) - __ldg(p.cu_k + seq);
+  s.ok = s.n > 0 && s.len >= s.n && s.len <= static_cast<long long>(p.maxb) * kBlockSize && q1 <= p.total_q &&
+         s.q0 >= 0 && s.n <= p.max_q && s.len <= p.max_k;
+  return s;
+}
+
+// K/V tiles that query tile `rank` (0 = last, the heaviest) of a sequence reads.
+__device__ __forceinline__ int kv_tiles(const Params& p, const Seq& s, int rank) {
+  const int tokens = kTileM >> p.log2_heads, ntiles = (s.n + tokens - 1) / tokens;
+  if (!s.ok || rank >= ntiles) return 0;
+  return (s.len - s.n + min((ntiles - rank) * tokens, s.n) + kTileN - 1) / kTileN;
+}
+
+constexpr int kMinPiece = 4;      // K/V tiles of a piece
+constexpr int kMaxSplitTiles = 160;  // query tiles (over all sequences) of a split call
+
+// Split mode: the query tile (sequence, rank) and piece of piece group `group`,
+// found by the whole warp.  False if there is none.
+__device__ bool find_piece(const Params& p, int group, int budget, int* seq, int* rank, int* piece, int* pieces) {
+  const int lane = threadIdx.x & 31, entries = p.S * p.tiles;
+  int kv[kMaxSplitTiles / 32];
+  int most = 0;
+#pragma unroll
+  for (int k = 0; k < kMaxSplitTiles / 32; ++k) {
+    const int e = 32 * k + lane;
+    kv[k] = e < entries ? kv_tiles(p, load_seq(p, e / p.tiles), e % p.tiles) : 0;
+    most = max(most, kv[k]);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  auto groups_at = [&](int c) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxSplitTiles / 32; ++k) n += (kv[k] + c - 1) / c;
+    return static_cast<int>(__reduce_add_sync(0xffffffffu, n));
+  };
+  int lo = kMinPiece, hi = max(most, kMinPiece);  // hi always fits: one piece a query tile
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (groups_at(mid) <= budget)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  int before = 0;
+#pragma unroll
+  for (int k = 0; k < kMaxSplitTiles / 32; ++k) {
+    const int mine = (kv[k] + lo - 1) / lo;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int first = before + incl - mine;
+    const unsigned hit = __ballot_sync(0xffffffffu, group >= first && group < first + mine);
+    if (hit) {
+      const int src = __ffs(hit) - 1, e = 32 * k + src;
+      *seq = e / p.tiles;
+      *rank = e % p.tiles;
+      *piece = group - __shfl_sync(0xffffffffu, first, src);
+      *pieces = __shfl_sync(0xffffffffu, mine, src);
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+enum Kinds { kBoth, kKeys, kValues };
+
+// Step `s` of a warpgroup that expands `kinds` of n tiles: the tile, and whether
+// it is V.  Both kinds go K(0), K(1), V(0), K(2), V(1), ...: the MMA warps need
+// K(j+1) (for the next S) before V(j) (for P V of j).
+template <Kinds kinds>
+__device__ __forceinline__ bool step_of(int s, int n, int* j) {
+  if (kinds != kBoth) {
+    *j = s;
+    return kinds == kValues;
+  }
+  if (s == 0 || s == 2 * n - 1) {
+    *j = s == 0 ? 0 : n - 1;
+    return s != 0;
+  }
+  const bool v = (s & 1) == 0;
+  *j = (s + 1) / 2 - (v ? 1 : 0);
+  return v;
+}
+
+constexpr int kAhead = 6;  // steps from a row's L2 prefetch to its use
+
+// Expand token `i` of this CTA's n tiles from tile j0 on into the rings, one step
+// fetched into registers while the one before is expanded.
+template <Kinds kinds>
+__device__ __forceinline__ void dequantise(const Params& p, const Smem& sm, const int32_t* table, int j0, int n, int i,
+                                           int g, int len) {
+  const int lane = threadIdx.x & 31, steps = kinds == kBoth ? 2 * n : n;
+  auto put = [&](int s, const Packed& x) {
+    int j;
+    const bool v = step_of<kinds>(s, n, &j);
+    const int st = v ? j % kVStages : j % kKStages;
+    const uint32_t par = ((v ? j / kVStages : j / kKStages) & 1) ^ 1;
+    if (!mbar_wait(v ? &sm.v_empty[st] : &sm.k_empty[st], par, &g_err_prefill_q4)) return false;
+    expand(x, smem_u32(v ? sm.v0 + st * kTileBytes : sm.k0 + st * kTileBytes), i);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(v ? &sm.v_full[st] : &sm.k_full[st]);
+    return true;
+  };
+  // Past the end the last step is fetched again: a fetch under a condition would
+  // make the registers wait for it where the paths join (15 % on long prompts).
+  auto get = [&](int s, Packed& x) {
+    int j;
+    const bool v = step_of<kinds>(min(s, steps - 1), n, &j);
+    fetch(p, table, j0 + j, v, i, g, len, x);
+    if (kinds != kBoth && s + kAhead < steps) {
+      const bool w = step_of<kinds>(s + kAhead, n, &j);
+      prefetch_row(p, table, j0 + j, w, i, g);
+    }
+  };
+  if (n == 0) return;
+  Packed a, b;
+  get(0, a);
+  for (int s = 0; s < steps; s += 2) {
+    get(s + 1, b);
+    if (!put(s, a)) break;
+    get(s + 2, a);
+    if ((kinds == kBoth || s + 1 < steps) && !put(s + 1, b)) break;
+  }
+}
+
+// kSplit: split mode.  (A template because a query tile found by the warp lives in
+// ordinary registers, one known from blockIdx in uniform ones: the common form
+// lost 15 % on long prompts to register pressure.)
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_q4_kernel(const __grid_constant__ CUtensorMap qmap, const Params p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int g = blockIdx.x / p.npairs;  // kv head
-  const int pair = blockIdx.x - g * p.npairs;
+  int unit = blockIdx.x, seq = blockIdx.y, rank = blockIdx.z, piece = 0, pieces = 1;
+  if (kSplit) {
+    const int units = p.Hkv * p.npairs, group = blockIdx.x / units;
+    unit = blockIdx.x - group * units;
+    if (!find_piece(p, group, gridDim.x / units, &seq, &rank, &piece, &pieces)) {
+      // Sequences out of bounds have no pieces: the last CTA reports them.
+      if (blockIdx.x == gridDim.x - 1 && threadIdx.x < 32)
+        for (int i = threadIdx.x; i < p.S; i += 32) {
+          const Seq s = load_seq(p, i);
+          if (!s.ok && s.n > 0) atomicOr(&g_err_prefill_q4, PKV_DEVERR_LEN_RANGE);
+        }
+      return;
+    }
+  }
+  const int g = unit / p.npairs;  // kv head
+  const int pair = unit - g * p.npairs;
   const bool has_b = 2 * pair + 1 < p.groups;  // slot B: the next group of heads
-  const int seq = blockIdx.y;
-  const int rank = blockIdx.z / p.splits, split = blockIdx.z - rank * p.splits;
-  const int q0 = __ldg(p.cu_q + seq), q1 = __ldg(p.cu_q + seq + 1);
-  const int k0 = __ldg(p.cu_k + seq), k1 = __ldg(p.cu_k + seq + 1);
-  const int n = q1 - q0, L = k1 - k0;
+  const Seq sq = load_seq(p, seq);
+  const int q0 = sq.q0, n = sq.n, L = sq.len;
   const int c = L - n;
-  if (n <= 0) return;
-  if (c < 0 || L > static_cast<long long>(p.maxb) * kBlockSize || q1 > p.total_q || q0 < 0 || n > p.max_q ||
-      L > p.max_k) {
-    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0) atomicOr(&g_err_prefill_q4, PKV_DEVERR_LEN_RANGE);
+  if (!sq.ok) {
+    if (n > 0 && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0)
+      atomicOr(&g_err_prefill_q4, PKV_DEVERR_LEN_RANGE);
     return;
   }
+  const int nkv_all = kv_tiles(p, sq, rank);
+  if (nkv_all == 0) return;
   const int tile_tokens = kTileM >> p.log2_heads;
-  const int ntiles = (n + tile_tokens - 1) / tile_tokens;
-  if (rank >= ntiles) return;
-  const int m = ntiles - 1 - rank;  // heaviest tile first
-  const int tok0 = tile_tokens * m;                       // first new token of the tile
-  const int kv_end = c + min(tok0 + tile_tokens, n);      // keys 0 .. kv_end-1 are visible to some row
-  const int nkv_all = (kv_end + kTileN - 1) / kTileN;
-  const int j0 = static_cast<int>(static_cast<int64_t>(nkv_all) * split / p.splits);
-  const int nkv = static_cast<int>(static_cast<int64_t>(nkv_all) * (split + 1) / p.splits) - j0;  // this CTA's K/V tiles
+  // rank 0 is the last query tile, the heaviest
+  const int tok0 = ((n + tile_tokens - 1) / tile_tokens - 1 - rank) * tile_tokens;  // first new token of the tile
+  const int j0 = static_cast<int>(static_cast<int64_t>(nkv_all) * piece / pieces);
+  const int nkv = static_cast<int>(static_cast<int64_t>(nkv_all) * (piece + 1) / pieces) - j0;  // this CTA's K/V tiles
+  if (kSplit && piece == 0 && unit == 0 && threadIdx.x == 0) p.ws_pieces[seq * p.tiles + rank] = pieces;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base =
@@ -245,6 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head0 = g * p.G + ((2 * pair) << p.log2_heads);  // first query head of slot A
 
+  // The first rows are on their way into L2 while the barriers and tensor memory
+  // are set up.
+  const int32_t* table = p.tables + static_cast<int64_t>(seq) * p.maxb;
+  if (nkv > 0 && warp >= 8) prefetch_row(p, table, j0, warp < 12, threadIdx.x & 127, g);
   if (threadIdx.x == 0) {
     prefetch_tensormap(&qmap);
     for (int i = 0; i < kKStages; ++i) {
@@ -349,7 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int slot = warp >= 8 ? 1 : 0;
-    if (slot == 0 || has_b) {
+    if (slot == 1 && !has_b) {
+      dequantise<kValues>(p, sm, table, j0, nkv, threadIdx.x - 256, g, L);
+    } else {
       // -------------------------------------------------------- softmax + epilogue
       const int wq = warp & 3;
       const int r = wq * 32 + lane;  // tile row = TMEM lane
@@ -437,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           alpha = fast_exp2(m_ref - m_new);  // 0 on the first tile (m_ref = -inf)
           m_ref = m_new;
         }
-        // A row that has seen no key yet (a split behind the diagonal) keeps -inf.
+        // A row that has seen no key yet (a piece behind the diagonal) keeps -inf.
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
         // p = 2^(s * sl - m) <= 2^8, packed to fp16 pairs
         float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -482,9 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int head = head0 + (slot << p.log2_heads) + (r & ((1 << p.log2_heads) - 1));
       const bool real = tok < n && head < (g + 1) * p.G;
-      if (p.splits > 1) {
-        // Partial result of this split; one without keys leaves a zero sum.
-        const int64_t at = (static_cast<int64_t>(split) * p.total_q + q0 + tok) * p.Hq + head;
+      if (kSplit) {
+        // Partial result of this piece.
+        const int64_t at = (static_cast<int64_t>(piece) * p.total_q + q0 + tok) * p.Hq + head;
         if (nkv > 0 && ok) ok = mbar_wait(&sm.o_done[slot], 0, &g_err_prefill_q4);
         if (real) p.ws_ml[at] = make_float2(l > 0.f || l != l ? m_ref : -FLT_MAX, ok ? l : 0.f);
         if (nkv > 0 && ok) {
@@ -540,52 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
-    // ---------------------------------------------------------- dequantisation
-    // Order K(0), K(1), V(0), K(2), V(1), ...: the MMA warps need K(j+1) (for
-    // the next S) before V(j) (for P V of j).
-    const int i = threadIdx.x - 384;  // token of the tile
-    const int32_t* table = p.tables + static_cast<int64_t>(seq) * p.maxb;
-    const int steps = 2 * nkv;
-    auto item = [&](int s, int* j) {  // true: V
-      if (s == 0) {
-        *j = 0;
-        return false;
-      }
-      if (s == steps - 1) {
-        *j = nkv - 1;
-        return true;
-      }
-      const bool v = (s & 1) == 0;
-      *j = (s + 1) / 2 - (v ? 1 : 0);
-      return v;
-    };
-    auto put = [&](int s, const Packed& x) {
-      int j;
-      const bool v = item(s, &j);
-      const int st = v ? j % kVStages : j % kKStages;
-      const uint32_t par = ((v ? j / kVStages : j / kKStages) & 1) ^ 1;
-      if (!mbar_wait(v ? &sm.v_empty[st] : &sm.k_empty[st], par, &g_err_prefill_q4)) return false;
-      expand(x, smem_u32(v ? sm.v0 + st * kTileBytes : sm.k0 + st * kTileBytes), i);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v ? &sm.v_full[st] : &sm.k_full[st]);
-      return true;
-    };
-    auto get = [&](int s, Packed& x) {
-      int j;
-      const bool v = item(s, &j);
-      fetch(p, table, j0 + j, v, i, g, L, x);
-    };
-    if (steps > 0) {
-      Packed a, b;
-      get(0, a);
-      for (int s = 0; s < steps; s += 2) {
-        get(s + 1, b);
-        if (!put(s, a)) break;
-        if (s + 2 < steps) get(s + 2, a);
-        if (!put(s + 1, b)) break;
-      }
-    }
+    if (has_b)
+      dequantise<kBoth>(p, sm, table, j0, nkv, threadIdx.x - 384, g, L);
+    else
+      dequantise<kKeys>(p, sm, table, j0, nkv, threadIdx.x - 384, g, L);
   }
   tc::fence_before();
   __syncthreads();
@@ -593,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tc::dealloc(tmem, kTmemCols);
 }
 
-// Join the splits' partial results: one warp per (token, head), lane i dims
+// Join the pieces' partial results: one warp per (token, head), lane i dims
 // 4i .. 4i+3.  Tokens that no valid sequence owns are left alone.
 constexpr int kCombineWarps = 4;
 
@@ -601,22 +734,22 @@ __global__ void __launch_bounds__(32 * kCombineWarps) prefill_q4_combine_kernel(
   griddep_wait();
   griddep_launch_dependents();
   const int seq = blockIdx.y, lane = threadIdx.x & 31;
-  const int q0 = __ldg(p.cu_q + seq), n = __ldg(p.cu_q + seq + 1) - q0;
-  const int L = __ldg(p.cu_k + seq + 1) - __ldg(p.cu_k + seq);
-  if (n <= 0 || L < n || L > static_cast<long long>(p.maxb) * kBlockSize || q0 + n > p.total_q || q0 < 0 ||
-      n > p.max_q || L > p.max_k)
-    return;
+  const Seq sq = load_seq(p, seq);
+  if (!sq.ok) return;
+  const int q0 = sq.q0, n = sq.n, tokens = kTileM >> p.log2_heads, ntiles = (n + tokens - 1) / tokens;
   const int64_t pairs = static_cast<int64_t>(n) * p.Hq;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5); i < pairs;
        i += static_cast<int64_t>(gridDim.x) * kCombineWarps) {
     const int64_t at = static_cast<int64_t>(q0) * p.Hq + i, step = static_cast<int64_t>(p.total_q) * p.Hq;
+    const int rank = ntiles - 1 - static_cast<int>(i / p.Hq) / tokens;
+    const int pieces = min(p.pieces, p.ws_pieces[seq * p.tiles + rank]);
     float M = -FLT_MAX;
-    for (int s = 0; s < p.splits; ++s) M = fmaxf(M, p.ws_ml[at + s * step].x);
+    for (int s = 0; s < pieces; ++s) M = fmaxf(M, p.ws_ml[at + s * step].x);
     float lsum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < p.splits; ++s) {
+    for (int s = 0; s < pieces; ++s) {
       const float2 ml = p.ws_ml[at + s * step];
-      if (ml.y == 0.f) continue;  // no key of this split is visible: nothing was written
+      if (ml.y == 0.f) continue;  // no key of this piece is visible: nothing was written
       const float w = fast_exp2(ml.x - M);
       const float4 v = *reinterpret_cast<const float4*>(p.ws_o + (at + s * step) * kHeadDim + 4 * lane);
       lsum += w * ml.y;
@@ -635,7 +768,8 @@ size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
 
 // How a call is laid out, from sizes that the host knows.
 struct Plan {
-  int log2_heads, groups, npairs, tiles, splits;
+  int log2_heads, groups, npairs, tiles;
+  int pieces;  // 0: one CTA per query tile; else split mode, the most pieces of a query tile
 };
 
 Plan plan_for(int num_seqs, int max_q, int max_k, int hq, int hkv, int num_sms) {
@@ -648,15 +782,27 @@ Plan plan_for(int num_seqs, int max_q, int max_k, int hq, int hkv, int num_sms) 
   a.npairs = (a.groups + 1) / 2;
   const int tokens = kTileM >> a.log2_heads;
   a.tiles = (max_q + tokens - 1) / tokens;
-  // Fewer CTAs than SMs: split the keys, at least four tiles (512 keys) to a split.
-  const int64_t ctas = static_cast<int64_t>(hkv) * a.npairs * num_seqs * a.tiles;
-  const int64_t most = std::max<int64_t>(1, (max_k + kTileN - 1) / kTileN / 4);
-  a.splits = ctas > 0 ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms / ctas, most))) : 1;
+  // Split mode when the SMs could take at least one more piece of every (head,
+  // pair) than there are query tiles and the contexts are long enough.
+  const int64_t tiles = static_cast<int64_t>(num_seqs) * a.tiles;
+  const int budget = num_sms / (hkv * a.npairs);
+  a.pieces = 0;
+  if (tiles > 0 && tiles < budget && tiles <= kMaxSplitTiles && max_k >= 2 * kMinPiece * kTileN)
+    a.pieces = std::min(budget, ((max_k + kTileN - 1) / kTileN + kMinPiece - 1) / kMinPiece);
   return a;
 }
 
-size_t ml_bytes(const Plan& a, int total_q, int hq) {
-  return align256(static_cast<size_t>(a.splits) * total_q * hq * sizeof(float2));
+struct WsLayout {
+  size_t ml, pieces, total;
+};
+
+WsLayout ws_layout(const Plan& a, int num_seqs, int total_q, int hq) {
+  WsLayout l;
+  const size_t rows = static_cast<size_t>(a.pieces) * total_q * hq;
+  l.ml = align256(rows * kHeadDim * sizeof(float));
+  l.pieces = l.ml + align256(rows * sizeof(float2));
+  l.total = l.pieces + align256(static_cast<size_t>(num_seqs) * a.tiles * sizeof(int32_t));
+  return l;
 }
 
 }  // namespace
@@ -664,22 +810,21 @@ size_t ml_bytes(const Plan& a, int total_q, int hq) {
 size_t prefill_q4_workspace_bytes(int total_q, int num_seqs, int max_seqlen_q, int max_seqlen_k, int num_q_heads,
                                   int num_kv_heads, int num_sms) {
   const Plan a = plan_for(num_seqs, max_seqlen_q, max_seqlen_k, num_q_heads, num_kv_heads, num_sms);
-  if (a.splits <= 1) return 256;
-  return ml_bytes(a, total_q, num_q_heads) +
-         static_cast<size_t>(a.splits) * total_q * num_q_heads * kHeadDim * sizeof(float);
+  return a.pieces ? ws_layout(a, num_seqs, total_q, num_q_heads).total : 256;
 }
 
 cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
   const Plan pl = plan_for(a.num_seqs, a.max_seqlen_q, a.max_seqlen_k, a.num_q_heads, a.cache.num_kv_heads, num_sms);
+  void (*kernel)(CUtensorMap, Params) = pl.pieces ? prefill_q4_kernel<true> : prefill_q4_kernel<false>;
   // The warpgroups' requests for registers can only be met if the kernel was
   // built with exactly the launch's share per thread.
-  static std::atomic<int> regs_checked{0};
-  if (!regs_checked.load(std::memory_order_acquire)) {
+  static std::atomic<int> regs_checked[2];
+  if (!regs_checked[pl.pieces > 0].load(std::memory_order_acquire)) {
     cudaFuncAttributes fa{};
-    const cudaError_t e = cudaFuncGetAttributes(&fa, prefill_q4_kernel);
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
-    regs_checked.store(1, std::memory_order_release);
+    regs_checked[pl.pieces > 0].store(1, std::memory_order_release);
   }
   CUtensorMap qmap;
   if (!encode_q4_query_map(a.q, a.total_q, a.num_q_heads, pl.log2_heads, &qmap)) return cudaErrorUnknown;
@@ -689,8 +834,11 @@ cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int num_sms, cudaS
   p.tables = a.block_tables;
   p.out = a.out;
   p.c = a.cache;
-  p.ws_ml = static_cast<float2*>(a.workspace);
-  p.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + ml_bytes(pl, a.total_q, a.num_q_heads));
+  const WsLayout wl = ws_layout(pl, a.num_seqs, a.total_q, a.num_q_heads);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.ws_o = reinterpret_cast<float*>(ws);
+  p.ws_ml = reinterpret_cast<float2*>(ws + wl.ml);
+  p.ws_pieces = reinterpret_cast<int32_t*>(ws + wl.pieces);
   p.maxb = a.max_blocks_per_seq;
   p.Hq = a.num_q_heads;
   p.Hkv = a.cache.num_kv_heads;
@@ -700,15 +848,17 @@ cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int num_sms, cudaS
   p.total_q = a.total_q;
   p.max_q = a.max_seqlen_q;
   p.max_k = a.max_seqlen_k;
-  p.splits = pl.splits;
+  p.pieces = pl.pieces;
+  p.tiles = pl.tiles;
+  p.S = a.num_seqs;
   p.log2_heads = pl.log2_heads;
   p.sl2 = a.scale * a.cache.k_scale * 1.4426950408889634f;
-  static std::atomic<int> smem_set[kMaxDevices];
-  cudaError_t e = ensure_dyn_smem(prefill_q4_kernel, kSmemBytes, smem_set);
+  static std::atomic<int> smem_set[2][kMaxDevices];
+  cudaError_t e = ensure_dyn_smem(kernel, kSmemBytes, smem_set[pl.pieces > 0]);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(prefill_q4_kernel, dim3(p.Hkv * pl.npairs, a.num_seqs, pl.tiles * pl.splits), dim3(kThreads),
-                 kSmemBytes, stream, qmap, p);
-  if (e != cudaSuccess || pl.splits <= 1) return e;
+  const dim3 grid = pl.pieces ? dim3(num_sms) : dim3(p.Hkv * pl.npairs, a.num_seqs, pl.tiles);
+  e = launch_pdl(kernel, grid, dim3(kThreads), kSmemBytes, stream, qmap, p);
+  if (e != cudaSuccess || !pl.pieces) return e;
   const int64_t pairs = static_cast<int64_t>(a.max_seqlen_q) * p.Hq;
   const unsigned x = static_cast<unsigned>(std::min<int64_t>((pairs + kCombineWarps - 1) / kCombineWarps, 4096));
   return launch_pdl(prefill_q4_combine_kernel, dim3(x, a.num_seqs), dim3(32 * kCombineWarps), 0, stream, p);
