@@ -1,4 +1,5 @@
-// decode_q4.cu -- one query token per sequence against the 4-bit cache.
+// decode_q4.cu -- one query token per sequence, or a few ("rows": the last tokens
+// of a prompt, drafted tokens to verify), against the 4-bit cache.
 //
 // Bound by HBM: a context token costs 144 bytes per kv head (codes and scales of
 // its K and V rows), 3.6 times less than in bf16, so the arithmetic that turns
@@ -29,6 +30,11 @@
 //   A byte of two codes becomes two fp16 values in one conversion and one
 //   multiplication by the scale (exact).  The query is scaled by a power of two
 //   per head (its largest element to 2^14 .. 2^15), undone in the softmax scale.
+// * A sequence's query rows of one kv head, (new token, head of the group) pairs,
+//   are the columns of both products, up to 8 NT.  With one token the operand of
+//   the first product stays in registers; with rows each lane keeps its part in
+//   shared memory, private to it, and the causal limit of each column is applied
+//   in the tiles that reach the new tokens.
 // * Softmax in log2 units.  The running maximum is raised only when a score
 //   exceeds it by 8 (p <= 2^8 is in range of fp16), which costs a vote per tile
 //   instead of a reduction; P^T is the transpose of S^T's fragment (movmatrix).
@@ -69,6 +75,10 @@ template <>
 struct Shape<2> {
   static constexpr int kConsumers = 8, kRegsLaunch = 168, kRegsConsumer = 216, kRegsProducer = 64;
 };
+template <>
+struct Shape<4> {
+  static constexpr int kConsumers = 8, kRegsLaunch = 168, kRegsConsumer = 224, kRegsProducer = 56;
+};
 template <int NT>
 constexpr int threads_of() {
   using S = Shape<NT>;
@@ -88,19 +98,22 @@ struct alignas(16) TileHeader {
 
 struct Params {
   const uint16_t* q;
-  const int32_t* ctx;
+  const int32_t* ctx;   // one token a sequence
+  const int32_t* cu_q;  // rows
+  const int32_t* cu_k;
+  int32_t max_q, total_q;
   const int32_t* tables;
   uint16_t* out;
   const uint8_t* k_scales;
   const uint8_t* v_scales;
-  float* ws_o;    // [slots, Hq, 128] unnormalised partial outputs
-  float2* ws_ml;  // [slots, Hq] (row max in log2 units, row sum)
+  float* ws_o;    // [slots, max_q, Hq, 128] unnormalised partial outputs
+  float2* ws_ml;  // [slots, max_q, Hq] (row max in log2 units, row sum)
   int2* ws_meta;  // [B] first and last CTA holding sequence b
   int32_t maxb, B, Hq, Hkv, G, num_blocks, lmax;
   int32_t log2_r, log2_tile, stages;  // R, T and the ring's depth
   float sl2;      // scale * k_scale * log2(e)
   float v_scale;
-  uint32_t data_bytes, scale_bytes, stage_bytes, q_slot_bytes;
+  uint32_t data_bytes, scale_bytes, stage_bytes, q_slot_bytes, q_bytes;
 };
 
 __device__ __forceinline__ int clamp_len(int L, int lmax) {
@@ -111,9 +124,23 @@ __device__ __forceinline__ int clamp_len(int L, int lmax) {
   return L;
 }
 
+// A sequence's length: keys to attend to, 0 for none.
+template <bool kRows>
+__device__ __forceinline__ int length_of(const Params& p, int b) {
+  if (!kRows) return __ldg(p.ctx + b);  // clamped by the caller
+  const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1), n = q1 - q0;
+  const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
+  if (n <= 0) return 0;
+  if (L < n || L > p.lmax || q0 < 0 || q1 > p.total_q || n > p.max_q) {
+    atomicOr(&g_err_decode_q4, PKV_DEVERR_LEN_RANGE);
+    return 0;
+  }
+  return L;
+}
+
 struct Smem {
   uint8_t* stages;
-  uint8_t* qbuf;
+  uint8_t* qbuf;   // staged query rows; with rows, the lanes' operands
   float* ex_o;     // [writer][value][lane]: a warp's output at a unit's end
   float2* ex_ml;   // [writer][head of the group]
   TileHeader* hdr;
@@ -129,7 +156,7 @@ __device__ __forceinline__ Smem carve(uint8_t* base, const Params& p, int nt) {
   const int writers = p.Hkv * ((1 << p.log2_r) - 1);
   s.stages = base;
   s.qbuf = base + p.stages * p.stage_bytes;
-  s.ex_o = reinterpret_cast<float*>(s.qbuf + kQSlots * p.q_slot_bytes);
+  s.ex_o = reinterpret_cast<float*>(s.qbuf + p.q_bytes);
   s.ex_ml = reinterpret_cast<float2*>(s.ex_o + writers * nt * 32 * 32);
   s.hdr = reinterpret_cast<TileHeader*>(s.ex_ml + writers * nt * 8);
   s.full = reinterpret_cast<uint64_t*>(s.hdr + kMaxStages);
@@ -169,6 +196,7 @@ __device__ __forceinline__ int load_block(const Params& p, int b, int lb) {
 
 // Issue every tile of unit (b, [lo, hi)), lo a multiple of the tile: R stages of
 // 32 tokens each.  Lane 0 of the producer warp only.
+template <bool kRows>
 __device__ void emit_unit(const Params& p, const Smem& sm, const CUtensorMap* kmap, const CUtensorMap* vmap,
                           ProducerState& ps, int b, int lo, int hi, int L, int first_phys) {
   int lb_cur = -1, phys = 0, nxt = first_phys;
@@ -186,7 +214,7 @@ __device__ void emit_unit(const Params& p, const Smem& sm, const CUtensorMap* km
     h.t0 = t;
     h.flags = (t < lo + tile ? kFirst : 0) | (t >= end - tile ? kLast : 0) | (lo == 0 && hi == L ? kWhole : 0);
     sm.hdr[st] = h;
-    if (t == lo) {
+    if (!kRows && t == lo) {
       const uint32_t qs = ps.units % kQSlots;
       if (!mbar_wait(&sm.qempty[qs], ((ps.units / kQSlots) & 1u) ^ 1u, &g_err_decode_q4)) {
         ps.ok = false;
@@ -233,6 +261,7 @@ __device__ __forceinline__ int warp_incl_scan(int x, int lane) {
   return x;
 }
 
+template <bool kRows>
 __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kmap, const CUtensorMap* vmap) {
   const int lane = threadIdx.x & 31;
   if (lane == 0) {
@@ -245,7 +274,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
   int len[8];
   auto load_lengths = [&](int base) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) len[i] = base + 32 * i + lane < p.B ? __ldg(p.ctx + base + 32 * i + lane) : 0;
+    for (int i = 0; i < 8; ++i) len[i] = base + 32 * i + lane < p.B ? length_of<kRows>(p, base + 32 * i + lane) : 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) len[i] = clamp_len(len[i], p.lmax);
   };
@@ -291,7 +320,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
         const int hij = __shfl_sync(0xffffffffu, hi_t, j);
         const int Lj = __shfl_sync(0xffffffffu, L, j);
         const int physj = __shfl_sync(0xffffffffu, first_phys, j);
-        if (lane == 0 && ps.ok) emit_unit(p, sm, kmap, vmap, ps, bj, loj, hij, Lj, physj);
+        if (lane == 0 && ps.ok) emit_unit<kRows>(p, sm, kmap, vmap, ps, bj, loj, hij, Lj, physj);
         ps.ok = __shfl_sync(0xffffffffu, ps.ok, 0);
       }
       S += __shfl_sync(0xffffffffu, incl, 31);
@@ -322,8 +351,8 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
 __device__ __forceinline__ uint32_t dup_lo(uint32_t h2) { return __byte_perm(h2, 0, 0x1010); }
 __device__ __forceinline__ uint32_t dup_hi(uint32_t h2) { return __byte_perm(h2, 0, 0x3232); }
 
-// NT: eights of query heads of a group (1 or 2).
-template <int NT>
+// NT: eights of columns (query heads of a group, times new tokens).
+template <int NT, bool kRows>
 __device__ void consumer(const Params& p, const Smem& sm) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = 1 << p.log2_r;
@@ -344,9 +373,13 @@ __device__ void consumer(const Params& p, const Smem& sm) {
   const uint32_t vsa = sbase + p.scale_bytes + ta * srow + g, vsb = sbase + p.scale_bytes + tb * srow + g;
   const float kLowest = -FLT_MAX;  // maximum of no scores: factors 2^(kLowest - m) are zero
 
-  uint32_t qb[NT][16];   // B operand of the first product: this lane's 32 dims of query head g (+ 8)
-  float acc[NT][8][4];   // O^T: dims 16g + 2i (0, 1) and 16g + 2i + 1 (2, 3) of heads 2c, 2c + 1
+  // B operand of the first product: this lane's 32 dims of column g (+ 8n)
+  uint32_t qb[kRows ? 1 : NT][16];
+  const uint32_t qf = smem_u32(sm.qbuf) + static_cast<uint32_t>((w * NT * 4 * 32 + lane) * 16);
+  int limit0 = 0;        // rows: keys that the first new token sees
+  float acc[NT][8][4];   // O^T: dims 16g + 2i (0, 1) and 16g + 2i + 1 (2, 3) of columns 2c, 2c + 1 (+ 8n)
   float sl[NT][2], m[NT][2], l[NT][2];
+  constexpr int U = NT == 4 ? 1 : 2;  // steps of 16 tokens taken together
   uint32_t stage = r, phase = 0, units = 0;
   const uint32_t ring = smem_u32(sm.stages);
 
@@ -356,34 +389,61 @@ __device__ void consumer(const Params& p, const Smem& sm) {
     if (hd.b < 0) return;
     if (hd.flags & kFirst) {
       const uint32_t qs = units % kQSlots;
-      if (!mbar_wait(&sm.qfull[qs], (units / kQSlots) & 1u, &g_err_decode_q4)) return;
+      int q0 = 0, columns = p.G;
+      if (kRows) {
+        q0 = __ldg(p.cu_q + hd.b);
+        const int n_new = __ldg(p.cu_q + hd.b + 1) - q0;
+        limit0 = __ldg(p.cu_k + hd.b + 1) - __ldg(p.cu_k + hd.b) - n_new + 1;
+        columns *= n_new;
+      } else if (!mbar_wait(&sm.qfull[qs], (units / kQSlots) & 1u, &g_err_decode_q4)) {
+        return;
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         // Two passes over the 64 bytes (the largest element first) keep few registers live.
-        const bool real = g + 8 * n < p.G;
-        const uint32_t src = smem_u32(sm.qbuf) + qs * p.q_slot_bytes +
-                             (h * p.G + (real ? g + 8 * n : 0)) * (kHeadDim * 2) + c * 64;
+        const bool real = g + 8 * n < columns;
+        const int col = real ? g + 8 * n : 0;
+        uint32_t src = 0;
+        const uint4* row = nullptr;
+        if (kRows) {
+          const int tok = col / p.G;
+          row = reinterpret_cast<const uint4*>(
+                    p.q + (static_cast<int64_t>(q0 + tok) * p.Hq + h * p.G + col - tok * p.G) * kHeadDim) + 4 * c;
+        } else {
+          src = smem_u32(sm.qbuf) + qs * p.q_slot_bytes + (h * p.G + col) * (kHeadDim * 2) + c * 64;
+        }
+        auto load = [&](int i) { return kRows ? __ldg(row + i) : lds128(src + 16 * i); };
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 a = lds128(src + 16 * i);
+          const uint4 a = load(i);
           top = fmax3(top, fmax3(fabsf(q4::bf_lo(a.x)), fabsf(q4::bf_hi(a.x)), fabsf(q4::bf_lo(a.y))),
                       fmax3(fabsf(q4::bf_hi(a.y)), fabsf(q4::bf_lo(a.z)), fabsf(q4::bf_hi(a.z))));
           top = fmax3(top, fabsf(q4::bf_lo(a.w)), fabsf(q4::bf_hi(a.w)));
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^(14 - e) for a largest element in [2^e, 2^(e+1)); 0 for a head that is not there
+        // 2^(14 - e) for a largest element in [2^e, 2^(e+1)); 0 for a column that is not there
         const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 15), 254);
         const float f = real ? __uint_as_float(static_cast<uint32_t>(268 - ex) << 23) : 0.f;
         const float inv = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 a = lds128(src + 16 * i);
-          qb[n][4 * i] = pack_f16x2(q4::bf_lo(a.x) * f, q4::bf_hi(a.x) * f);
-          qb[n][4 * i + 1] = pack_f16x2(q4::bf_lo(a.y) * f, q4::bf_hi(a.y) * f);
-          qb[n][4 * i + 2] = pack_f16x2(q4::bf_lo(a.z) * f, q4::bf_hi(a.z) * f);
-          qb[n][4 * i + 3] = pack_f16x2(q4::bf_lo(a.w) * f, q4::bf_hi(a.w) * f);
+          const uint4 a = load(i);
+          const uint32_t x0 = pack_f16x2(q4::bf_lo(a.x) * f, q4::bf_hi(a.x) * f);
+          const uint32_t x1 = pack_f16x2(q4::bf_lo(a.y) * f, q4::bf_hi(a.y) * f);
+          const uint32_t x2 = pack_f16x2(q4::bf_lo(a.z) * f, q4::bf_hi(a.z) * f);
+          const uint32_t x3 = pack_f16x2(q4::bf_lo(a.w) * f, q4::bf_hi(a.w) * f);
+          if (kRows) {
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qf + (n * 4 + i) * 512), "r"(x0), "r"(x1),
+                         "r"(x2), "r"(x3)
+                         : "memory");
+          } else {
+            qb[kRows ? 0 : n][4 * i] = x0;
+            qb[kRows ? 0 : n][4 * i + 1] = x1;
+            qb[kRows ? 0 : n][4 * i + 2] = x2;
+            qb[kRows ? 0 : n][4 * i + 3] = x3;
+          }
         }
         sl[n][0] = p.sl2 * __shfl_sync(0xffffffffu, inv, 8 * c);
         sl[n][1] = p.sl2 * __shfl_sync(0xffffffffu, inv, 8 * c + 4);
@@ -393,122 +453,177 @@ __device__ void consumer(const Params& p, const Smem& sm) {
         for (int i = 0; i < 8; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.qempty[qs]);
+      if (!kRows && lane == 0) mbar_arrive(&sm.qempty[qs]);
     }
-    const int left = hd.hi - hd.t0;  // real tokens of the 32
-    if (left > 0) {
-      const uint32_t sb = ring + stage * p.stage_bytes;
-      // S^T = K Q^T for the two steps of 16 tokens
-      float s[NT][2][4];
+    if (hd.t0 < hd.hi) {
+      // Both steps of 16 tokens together, or, with many columns, one after the other.
+#pragma unroll 1
+      for (int part = 0; part < 2 / U; ++part) {
+        const uint32_t sb = ring + stage * p.stage_bytes + part * 1024;    // codes
+        const uint32_t ss = ring + stage * p.stage_bytes + part * 16 * srow;  // scales
+        const int left = hd.hi - hd.t0 - 16 * part;  // real tokens from here on
+        // S^T = K Q^T
+        float s[NT][U][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint4 ka = lds128(sb + ko + u * 1024), kb = lds128(sb + ko + u * 1024 + 512);  // rows tau(g), + 8
-        const uint32_t fa = q4::dec_scale2(lds_u16(sb + kso + u * 16 * srow));
-        const uint32_t fb = q4::dec_scale2(lds_u16(sb + kso + u * 16 * srow + 8 * srow));
+        for (int u = 0; u < U; ++u) {
+          const uint4 ka = lds128(sb + ko + u * 1024), kb = lds128(sb + ko + u * 1024 + 512);  // rows tau(g), + 8
+          const uint32_t fa = q4::dec_scale2(lds_u16(ss + kso + u * 16 * srow));
+          const uint32_t fb = q4::dec_scale2(lds_u16(ss + kso + u * 16 * srow + 8 * srow));
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s[n][u][0] = s[n][u][1] = s[n][u][2] = s[n][u][3] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t wa = i == 0 ? ka.x : i == 1 ? ka.y : i == 2 ? ka.z : ka.w;
-          const uint32_t wb = i == 0 ? kb.x : i == 1 ? kb.y : i == 2 ? kb.z : kb.w;
-          const uint32_t ea = i < 2 ? dup_lo(fa) : dup_hi(fa), eb = i < 2 ? dup_lo(fb) : dup_hi(fb);
-          uint32_t a[4], b[4];
-          q4::dec8(wa, a);
-          q4::dec8(wb, b);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a[j] = q4::hmul2(a[j], ea);
-            b[j] = q4::hmul2(b[j], eb);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_f16_16816(s[n][u], a[0], b[0], a[1], b[1], qb[n][4 * i], qb[n][4 * i + 1]);
-            mma_f16_16816(s[n][u], a[2], b[2], a[3], b[3], qb[n][4 * i + 2], qb[n][4 * i + 3]);
-          }
-        }
-      }
-      const bool ragged = left < kStepTokens;
-      uint32_t pb[NT][2][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (ragged) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (16 * u + tg >= left) s[n][u][0] = s[n][u][1] = -INFINITY;
-            if (16 * u + tg + 8 >= left) s[n][u][2] = s[n][u][3] = -INFINITY;
-          }
-        }
-        const float y0 = fmaxf(fmax3(s[n][0][0], s[n][0][2], s[n][1][0]), s[n][1][2]) * sl[n][0];
-        const float y1 = fmaxf(fmax3(s[n][0][1], s[n][0][3], s[n][1][1]), s[n][1][3]) * sl[n][1];
-        if (__any_sync(0xffffffffu, y0 > m[n][0] + 8.f || y1 > m[n][1] + 8.f)) {
-          float n0 = y0, n1 = y1;
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
-            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
-          }
-          n0 = fmaxf(n0, m[n][0]);
-          n1 = fmaxf(n1, m[n][1]);
-          const float a0 = fast_exp2(m[n][0] - n0), a1 = fast_exp2(m[n][1] - n1);
-          m[n][0] = n0;
-          m[n][1] = n1;
-          l[n][0] *= a0;
-          l[n][1] *= a1;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[n][i][0] *= a0;
-            acc[n][i][1] *= a1;
-            acc[n][i][2] *= a0;
-            acc[n][i][3] *= a1;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float p0 = fast_exp2(fmaf(s[n][u][0], sl[n][0], -m[n][0]));
-          const float p1 = fast_exp2(fmaf(s[n][u][1], sl[n][1], -m[n][1]));
-          const float p2 = fast_exp2(fmaf(s[n][u][2], sl[n][0], -m[n][0]));
-          const float p3 = fast_exp2(fmaf(s[n][u][3], sl[n][1], -m[n][1]));
-          l[n][0] += p0 + p2;
-          l[n][1] += p1 + p3;
-          pb[n][u][0] = movmatrix_trans(pack_f16x2(p0, p1));
-          pb[n][u][1] = movmatrix_trans(pack_f16x2(p2, p3));
-        }
-      }
-      // O^T += V^T P^T
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        // V words and scales of tokens tau(2c), tau(2c + 1), + 8
-        const uint2 v0 = lds64(sb + va + u * 1024), v1 = lds64(sb + vb + u * 1024);
-        const uint2 v2 = lds64(sb + va + u * 1024 + 512), v3 = lds64(sb + vb + u * 1024 + 512);
-        uint32_t s0 = lds_u8(sb + vsa + u * 16 * srow), s1 = lds_u8(sb + vsb + u * 16 * srow);
-        uint32_t s2 = lds_u8(sb + vsa + (u * 16 + 8) * srow), s3 = lds_u8(sb + vsb + (u * 16 + 8) * srow);
-        if (u == 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.empty[stage]);
-        }
-        if (ragged) {
-          if (16 * u + ta >= left) s0 = 0;
-          if (16 * u + tb >= left) s1 = 0;
-          if (16 * u + ta + 8 >= left) s2 = 0;
-          if (16 * u + tb + 8 >= left) s3 = 0;
-        }
-        const uint32_t e01 = q4::dec_scale2(s0 | s1 << 8), e23 = q4::dec_scale2(s2 | s3 << 8);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t a0 = half ? v0.y : v0.x, a1 = half ? v1.y : v1.x;
-          const uint32_t a2 = half ? v2.y : v2.x, a3 = half ? v3.y : v3.x;
-          const uint32_t kLow = 0x0f0f0f0fu;
-          uint32_t ev0[4], od0[4], ev1[4], od1[4];
-          q4::dec8((a0 & kLow) | ((a1 << 4) & ~kLow), ev0);
-          q4::dec8(((a0 >> 4) & kLow) | (a1 & ~kLow), od0);
-          q4::dec8((a2 & kLow) | ((a3 << 4) & ~kLow), ev1);
-          q4::dec8(((a2 >> 4) & kLow) | (a3 & ~kLow), od1);
+          for (int n = 0; n < NT; ++n) s[n][u][0] = s[n][u][1] = s[n][u][2] = s[n][u][3] = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t f0 = q4::hmul2(ev0[i], e01), f1 = q4::hmul2(od0[i], e01);
-            const uint32_t f2 = q4::hmul2(ev1[i], e23), f3 = q4::hmul2(od1[i], e23);
+            const uint32_t wa = i == 0 ? ka.x : i == 1 ? ka.y : i == 2 ? ka.z : ka.w;
+            const uint32_t wb = i == 0 ? kb.x : i == 1 ? kb.y : i == 2 ? kb.z : kb.w;
+            const uint32_t ea = i < 2 ? dup_lo(fa) : dup_hi(fa), eb = i < 2 ? dup_lo(fb) : dup_hi(fb);
+            uint32_t a[4], b[4];
+            q4::dec8(wa, a);
+            q4::dec8(wb, b);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16_16816(acc[n][4 * half + i], f0, f1, f2, f3, pb[n][u][0], pb[n][u][1]);
+            for (int j = 0; j < 4; ++j) {
+              a[j] = q4::hmul2(a[j], ea);
+              b[j] = q4::hmul2(b[j], eb);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint4 x = kRows ? lds128(qf + (n * 4 + i) * 512)
+                                    : make_uint4(qb[kRows ? 0 : n][4 * i], qb[kRows ? 0 : n][4 * i + 1],
+                                                 qb[kRows ? 0 : n][4 * i + 2], qb[kRows ? 0 : n][4 * i + 3]);
+              mma_f16_16816(s[n][u], a[0], b[0], a[1], b[1], x.x, x.y);
+              mma_f16_16816(s[n][u], a[2], b[2], a[3], b[3], x.z, x.w);
+            }
+          }
+        }
+        const int first = hd.t0 + 16 * part;
+        const bool ragged = left < 16 * U || (kRows && first + 16 * U > limit0);
+        if (kRows && ragged) {
+          // A NaN among a token's V scales goes into the token's scores (and its
+          // group's scale becomes zero below), so that it stays with the columns
+          // that see the token.
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const uint2 x = lds64(ss + sbase + p.scale_bytes + (16 * u + 8 * v + tg) * srow);
+              if (q4::nan_bytes(x.x) | q4::nan_bytes(x.y)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[n][u][2 * v] = s[n][u][2 * v + 1] = __uint_as_float(0x7fffffffu);
+              }
+            }
+        }
+        float y0[NT], y1[NT];  // largest scores of the lane's tokens
+        bool raise = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (kRows && ragged) {
+            // keys that columns 2c and 2c + 1 (+ 8n) see, from the stage's first on
+            const int see0 = limit0 + (8 * n + 2 * c) / p.G - first, see1 = limit0 + (8 * n + 2 * c + 1) / p.G - first;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                if (16 * u + 8 * v + tg >= min(see0, left)) s[n][u][2 * v] = -INFINITY;
+                if (16 * u + 8 * v + tg >= min(see1, left)) s[n][u][2 * v + 1] = -INFINITY;
+              }
+          } else if (ragged) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              if (16 * u + tg >= left) s[n][u][0] = s[n][u][1] = -INFINITY;
+              if (16 * u + tg + 8 >= left) s[n][u][2] = s[n][u][3] = -INFINITY;
+            }
+          }
+          y0[n] = fmaxf(s[n][0][0], s[n][0][2]);
+          y1[n] = fmaxf(s[n][0][1], s[n][0][3]);
+          if (U == 2) {
+            y0[n] = fmax3(y0[n], s[n][U - 1][0], s[n][U - 1][2]);
+            y1[n] = fmax3(y1[n], s[n][U - 1][1], s[n][U - 1][3]);
+          }
+          y0[n] *= sl[n][0];
+          y1[n] *= sl[n][1];
+          raise |= y0[n] > m[n][0] + 8.f || y1[n] > m[n][1] + 8.f;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float n0 = y0[n], n1 = y1[n];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
+              n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
+            }
+            n0 = fmaxf(n0, m[n][0]);
+            n1 = fmaxf(n1, m[n][1]);
+            const float a0 = fast_exp2(m[n][0] - n0), a1 = fast_exp2(m[n][1] - n1);
+            m[n][0] = n0;
+            m[n][1] = n1;
+            l[n][0] *= a0;
+            l[n][1] *= a1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[n][i][0] *= a0;
+              acc[n][i][1] *= a1;
+              acc[n][i][2] *= a0;
+              acc[n][i][3] *= a1;
+            }
+          }
+        }
+        uint32_t pb[NT][U][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const float p0 = fast_exp2(fmaf(s[n][u][0], sl[n][0], -m[n][0]));
+            const float p1 = fast_exp2(fmaf(s[n][u][1], sl[n][1], -m[n][1]));
+            const float p2 = fast_exp2(fmaf(s[n][u][2], sl[n][0], -m[n][0]));
+            const float p3 = fast_exp2(fmaf(s[n][u][3], sl[n][1], -m[n][1]));
+            l[n][0] += p0 + p2;
+            l[n][1] += p1 + p3;
+            pb[n][u][0] = movmatrix_trans(pack_f16x2(p0, p1));
+            pb[n][u][1] = movmatrix_trans(pack_f16x2(p2, p3));
+          }
+        }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          // V words and scales of tokens tau(2c), tau(2c + 1), + 8
+          const uint2 v0 = lds64(sb + va + u * 1024), v1 = lds64(sb + vb + u * 1024);
+          const uint2 v2 = lds64(sb + va + u * 1024 + 512), v3 = lds64(sb + vb + u * 1024 + 512);
+          uint32_t s0 = lds_u8(ss + vsa + u * 16 * srow), s1 = lds_u8(ss + vsb + u * 16 * srow);
+          uint32_t s2 = lds_u8(ss + vsa + (u * 16 + 8) * srow), s3 = lds_u8(ss + vsb + (u * 16 + 8) * srow);
+          if (u == U - 1 && part == 2 / U - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[stage]);
+          }
+          if (ragged) {
+            if (16 * u + ta >= left) s0 = 0;
+            if (16 * u + tb >= left) s1 = 0;
+            if (16 * u + ta + 8 >= left) s2 = 0;
+            if (16 * u + tb + 8 >= left) s3 = 0;
+            if (kRows) {
+              if ((s0 & 0x7f) == 0x7f) s0 = 0;
+              if ((s1 & 0x7f) == 0x7f) s1 = 0;
+              if ((s2 & 0x7f) == 0x7f) s2 = 0;
+              if ((s3 & 0x7f) == 0x7f) s3 = 0;
+            }
+          }
+          const uint32_t e01 = q4::dec_scale2(s0 | s1 << 8), e23 = q4::dec_scale2(s2 | s3 << 8);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t a0 = half ? v0.y : v0.x, a1 = half ? v1.y : v1.x;
+            const uint32_t a2 = half ? v2.y : v2.x, a3 = half ? v3.y : v3.x;
+            const uint32_t kLow = 0x0f0f0f0fu;
+            uint32_t ev0[4], od0[4], ev1[4], od1[4];
+            q4::dec8((a0 & kLow) | ((a1 << 4) & ~kLow), ev0);
+            q4::dec8(((a0 >> 4) & kLow) | (a1 & ~kLow), od0);
+            q4::dec8((a2 & kLow) | ((a3 << 4) & ~kLow), ev1);
+            q4::dec8(((a2 >> 4) & kLow) | (a3 & ~kLow), od1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t f0 = q4::hmul2(ev0[i], e01), f1 = q4::hmul2(od0[i], e01);
+              const uint32_t f2 = q4::hmul2(ev1[i], e23), f3 = q4::hmul2(od1[i], e23);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_f16_16816(acc[n][4 * half + i], f0, f1, f2, f3, pb[n][u][0], pb[n][u][1]);
+            }
           }
         }
       }
@@ -569,14 +684,20 @@ __device__ void consumer(const Params& p, const Smem& sm) {
           if (lane == 0) mbar_arrive(&sm.xempty[h]);
         }
         const bool whole = hd.flags & kWhole;
-        const int64_t row = whole ? hd.b : hd.b + static_cast<int>(blockIdx.x);
+        const int64_t slot = hd.b + static_cast<int>(blockIdx.x);
+        int q0 = hd.b, columns = p.G;
+        if (kRows) {
+          q0 = __ldg(p.cu_q + hd.b);
+          columns *= __ldg(p.cu_q + hd.b + 1) - q0;
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int head = 8 * n + 2 * c + k;
-            if (head >= p.G) continue;
-            const int64_t at = row * p.Hq + h * p.G + head;
+            const int col = 8 * n + 2 * c + k;
+            if (col >= columns) continue;
+            const int tok = kRows ? col / p.G : 0;
+            const int64_t at = (whole ? q0 + tok : slot * p.max_q + tok) * p.Hq + h * p.G + col - tok * p.G;
             if (whole) {
               const float inv = p.v_scale / l[n][k];
               uint32_t o[8];
@@ -604,7 +725,7 @@ __device__ void consumer(const Params& p, const Smem& sm) {
   }
 }
 
-template <int NT>
+template <int NT, bool kRows>
 __global__ void __launch_bounds__(threads_of<NT>(), 1)
     decode_q4_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const Params p) {
@@ -633,59 +754,85 @@ __global__ void __launch_bounds__(threads_of<NT>(), 1)
   using S = Shape<NT>;
   if (warp >= S::kConsumers) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsProducer));
-    if (warp == S::kConsumers) producer(p, sm, &kmap, &vmap);
+    if (warp == S::kConsumers) producer<kRows>(p, sm, &kmap, &vmap);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsConsumer));
-    if (warp < (p.Hkv << p.log2_r)) consumer<NT>(p, sm);
+    if (warp < (p.Hkv << p.log2_r)) consumer<NT, kRows>(p, sm);
   }
 }
 
-// Merge the partials of sequences that straddle CTAs; zero pad rows.  One warp
-// per (sequence, query head), lane i dims 4i .. 4i+3; the lanes share the pass
-// over the partials' maxima and sums.
+// Merge the partials of sequences that straddle CTAs; zero pad rows (one token a
+// sequence; with rows, what no valid sequence owns is left alone).  One warp per
+// query row and head, lane i dims 4i .. 4i+3; the lanes share the pass over the
+// partials' maxima and weights.
 constexpr int kCombineWarps = 4;
 
+template <bool kRows>
 __global__ void __launch_bounds__(32 * kCombineWarps) combine_q4_kernel(const Params p, int grid) {
   griddep_wait();
   griddep_launch_dependents();
   const int64_t pair = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
-  if (pair >= static_cast<int64_t>(p.B) * p.Hq) return;
-  const int b = static_cast<int>(pair / p.Hq), hq = static_cast<int>(pair - static_cast<int64_t>(b) * p.Hq);
+  // row: of one token a sequence the sequence, else row `tok` of sequence blockIdx.y
+  const int row = static_cast<int>(pair / p.Hq), hq = static_cast<int>(pair - static_cast<int64_t>(row) * p.Hq);
   const int lane = threadIdx.x & 31;
-  const int L_in = __ldg(p.ctx + b);
+  const int b = kRows ? blockIdx.y : row, tok = kRows ? row : 0;
+  if (kRows ? tok >= p.max_q : b >= p.B) return;
+  int first = b;
+  if (kRows) {
+    first = __ldg(p.cu_q + b);
+    if (tok >= __ldg(p.cu_q + b + 1) - first) return;
+    first += tok;
+  }
+  const int L_in = length_of<kRows>(p, b);
   const int2 meta = p.ws_meta[b];  // read only when the length is positive, i.e. when it was written
   const int L = clamp_len(L_in, p.lmax);
-  uint16_t* o = p.out + pair * kHeadDim + 4 * lane;
+  if (kRows && L == 0) return;
+  uint16_t* o = p.out + (static_cast<int64_t>(first) * p.Hq + hq) * kHeadDim + 4 * lane;
   if (L == 0) {
     *reinterpret_cast<uint2*>(o) = make_uint2(0u, 0u);
     return;
   }
   const int c0 = max(0, meta.x), c1 = min(grid - 1, meta.y);
   if (c1 <= c0) return;  // finished inside one CTA
-  float M = -FLT_MAX, lsum = 0.f;
-  for (int c = c0 + lane; c <= c1; c += 32) {
-    const float2 ml = p.ws_ml[static_cast<int64_t>(b + c) * p.Hq + hq];
-    const float n = fmaxf(M, ml.x);
-    lsum = lsum * fast_exp2(M - n) + ml.y * fast_exp2(ml.x - n);
-    M = n;
-  }
-  float top = M;
+  // The lanes share the pass over the maxima; then the weights come from the lane
+  // that holds a partial, with the outputs of eight partials in flight.
+  const int64_t step = static_cast<int64_t>(p.max_q) * p.Hq;
+  const int64_t at0 = (static_cast<int64_t>(b) * p.max_q + tok) * p.Hq + hq;
+  float top = -FLT_MAX;
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.ws_ml[at0 + c * step].x);
 #pragma unroll
   for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  lsum *= fast_exp2(M - top);
+  float lsum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int base = c0; base <= c1; base += 32) {
+    float w = 0.f;
+    if (base + lane <= c1) {
+      const float2 ml = p.ws_ml[at0 + (base + lane) * step];
+      w = fast_exp2(ml.x - top);
+      lsum += w * ml.y;
+    }
+    const int n = min(32, c1 - base + 1);
+    const float4* src = reinterpret_cast<const float4*>(p.ws_o + (at0 + base * step) * kHeadDim) + lane;
+    const int64_t hop = step * (kHeadDim / 4);
+    for (int i = 0; i < n; i += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v[k] = i + k < n ? src[(i + k) * hop] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float x = __shfl_sync(0xffffffffu, w, (i + k) & 31);
+        if (i + k < n) {
+          acc.x += x * v[k].x;
+          acc.y += x * v[k].y;
+          acc.z += x * v[k].z;
+          acc.w += x * v[k].w;
+        }
+      }
+    }
+  }
 #pragma unroll
   for (int s = 16; s; s >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, s);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const int64_t row = static_cast<int64_t>(b + c) * p.Hq + hq;
-    const float wgt = fast_exp2(p.ws_ml[row].x - top);
-    const float4 v = *reinterpret_cast<const float4*>(p.ws_o + row * kHeadDim + 4 * lane);
-    acc.x += wgt * v.x;
-    acc.y += wgt * v.y;
-    acc.z += wgt * v.z;
-    acc.w += wgt * v.w;
-  }
   const float inv = p.v_scale / lsum;
   *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
@@ -695,32 +842,39 @@ size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
 // How a call is laid out on the GPU.
 struct Plan {
   int nt, log2_r, stages;
-  uint32_t data_bytes, scale_bytes, stage_bytes, q_slot_bytes;
+  uint32_t data_bytes, scale_bytes, stage_bytes, q_slot_bytes, q_bytes;
   size_t smem;
 };
 
-Plan plan_for(int hq, int hkv) {
+// max_q: new tokens of a sequence at most (rows), or 0 for the one-token form.
+Plan plan_for(int hq, int hkv, int max_q) {
   Plan a;
-  a.nt = hq > 8 * hkv ? 2 : 1;
+  const int columns = (hq + hkv - 1) / hkv * std::max(1, max_q);
+  a.nt = columns > 16 ? 4 : columns > 8 ? 2 : 1;
   const int most = a.nt == 1 ? Shape<1>::kConsumers : Shape<2>::kConsumers;
-  a.log2_r = 0;
-  while (a.log2_r < kMaxLog2R && (hkv << (a.log2_r + 1)) <= most) ++a.log2_r;
+  static_assert(Shape<2>::kConsumers == Shape<4>::kConsumers, "consumer warps");
   a.data_bytes = static_cast<uint32_t>(kStepTokens * hkv * q4::kRowBytes);
   a.scale_bytes = static_cast<uint32_t>(kStepTokens * hkv * q4::kRowScales);
   a.stage_bytes = (2 * (a.data_bytes + a.scale_bytes) + 1023) & ~1023u;
   a.q_slot_bytes = static_cast<uint32_t>(hq * kHeadDim * 2);
-  const size_t rest = kFixedBytes + kQSlots * a.q_slot_bytes + hkv * ((1 << a.log2_r) - 1) * exchange_bytes(a.nt);
-  a.stages = static_cast<int>(std::min<size_t>(kMaxStages, (kSmemMax - rest) / a.stage_bytes));
-  a.smem = rest + static_cast<size_t>(a.stages) * a.stage_bytes;
-  return a;
+  // As many warps a kv head as there are, unless the room for merging them would
+  // leave fewer than four stages.
+  for (a.log2_r = kMaxLog2R;; --a.log2_r) {
+    const int warps = hkv << a.log2_r;
+    a.q_bytes = max_q ? static_cast<uint32_t>(warps * a.nt * 4 * 512) : kQSlots * a.q_slot_bytes;
+    const size_t rest = kFixedBytes + a.q_bytes + static_cast<size_t>(warps - hkv) * exchange_bytes(a.nt);
+    a.stages = rest < kSmemMax ? static_cast<int>(std::min<size_t>(kMaxStages, (kSmemMax - rest) / a.stage_bytes)) : 0;
+    a.smem = rest + static_cast<size_t>(a.stages) * a.stage_bytes;
+    if (a.log2_r == 0 || (warps <= most && a.stages >= std::max(3, 1 << a.log2_r))) return a;
+  }
 }
 
 struct WsLayout {
   size_t ml, meta, total;
 };
 
-WsLayout ws_layout(int batch, int num_q_heads, int grid) {
-  const size_t slots = static_cast<size_t>(batch) + grid;
+WsLayout ws_layout(int batch, int max_q, int num_q_heads, int grid) {
+  const size_t slots = (static_cast<size_t>(batch) + grid) * max_q;
   WsLayout l;
   l.ml = align256(slots * num_q_heads * kHeadDim * sizeof(float));
   l.meta = l.ml + align256(slots * num_q_heads * sizeof(float2));
@@ -728,7 +882,7 @@ WsLayout ws_layout(int batch, int num_q_heads, int grid) {
   return l;
 }
 
-template <int NT>
+template <int NT, bool kRows>
 cudaError_t launch(const Plan& pl, const Params& p, const CUtensorMap& km, const CUtensorMap& vm, int grid,
                    cudaStream_t stream) {
   // The warpgroups' requests for registers can only be met if the kernel was
@@ -736,33 +890,32 @@ cudaError_t launch(const Plan& pl, const Params& p, const CUtensorMap& km, const
   static std::atomic<int> regs_checked{0};
   if (!regs_checked.load(std::memory_order_acquire)) {
     cudaFuncAttributes fa{};
-    const cudaError_t e = cudaFuncGetAttributes(&fa, decode_q4_kernel<NT>);
+    const cudaError_t e = cudaFuncGetAttributes(&fa, decode_q4_kernel<NT, kRows>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != Shape<NT>::kRegsLaunch) return cudaErrorInvalidKernelImage;
     regs_checked.store(1, std::memory_order_release);
   }
   static std::atomic<int> smem_set[kMaxDevices];
-  const cudaError_t e = ensure_dyn_smem(decode_q4_kernel<NT>, pl.smem, smem_set);
+  const cudaError_t e = ensure_dyn_smem(decode_q4_kernel<NT, kRows>, pl.smem, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_q4_kernel<NT>, dim3(grid), dim3(threads_of<NT>()), pl.smem, stream, km, vm, p);
+  return launch_pdl(decode_q4_kernel<NT, kRows>, dim3(grid), dim3(threads_of<NT>()), pl.smem, stream, km, vm, p);
 }
 
-}  // namespace
-
-size_t decode_q4_workspace_bytes(int batch, int num_q_heads, int, int num_sms) {
-  return ws_layout(batch, num_q_heads, num_sms).total;
-}
-
-cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
-  const Plan pl = plan_for(a.num_q_heads, a.cache.num_kv_heads);
+// Shared by the one-token form (max_q 0) and the rows.
+cudaError_t launch_stream(const AttnQ4Args& a, int max_q, int num_sms, cudaStream_t stream) {
+  const Plan pl = plan_for(a.num_q_heads, a.cache.num_kv_heads, max_q);
   const int grid = num_sms;
-  const WsLayout wl = ws_layout(a.num_seqs, a.num_q_heads, grid);
+  const WsLayout wl = ws_layout(a.num_seqs, std::max(1, max_q), a.num_q_heads, grid);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   CUtensorMap km, vm;
   if (!encode_q4_maps(a.cache, kStepTokens, a.cache.num_kv_heads, &km, &vm)) return cudaErrorUnknown;
   Params p = {};
   p.q = a.q;
   p.ctx = a.context_lens;
+  p.cu_q = a.cu_seqlens_q;
+  p.cu_k = a.cu_seqlens_k;
+  p.max_q = std::max(1, max_q);
+  p.total_q = a.total_q;
   p.tables = a.block_tables;
   p.out = a.out;
   p.k_scales = a.cache.k_scales;
@@ -786,11 +939,38 @@ cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaSt
   p.scale_bytes = pl.scale_bytes;
   p.stage_bytes = pl.stage_bytes;
   p.q_slot_bytes = pl.q_slot_bytes;
-  const cudaError_t e = pl.nt == 1 ? launch<1>(pl, p, km, vm, grid, stream) : launch<2>(pl, p, km, vm, grid, stream);
+  p.q_bytes = pl.q_bytes;
+  auto go = max_q == 0 ? (pl.nt == 1 ? launch<1, false> : launch<2, false>)
+                       : (pl.nt == 1 ? launch<1, true> : pl.nt == 2 ? launch<2, true> : launch<4, true>);
+  const cudaError_t e = go(pl, p, km, vm, grid, stream);
   if (e != cudaSuccess) return e;
-  const int64_t pairs = static_cast<int64_t>(p.B) * p.Hq;
-  return launch_pdl(combine_q4_kernel, dim3(static_cast<unsigned>((pairs + kCombineWarps - 1) / kCombineWarps)),
-                    dim3(32 * kCombineWarps), 0, stream, p, grid);
+  const int64_t pairs = static_cast<int64_t>(max_q ? max_q : p.B) * p.Hq;
+  const unsigned x = static_cast<unsigned>((pairs + kCombineWarps - 1) / kCombineWarps);
+  if (max_q)
+    return launch_pdl(combine_q4_kernel<true>, dim3(x, p.B), dim3(32 * kCombineWarps), 0, stream, p, grid);
+  return launch_pdl(combine_q4_kernel<false>, dim3(x), dim3(32 * kCombineWarps), 0, stream, p, grid);
+}
+
+}  // namespace
+
+size_t decode_q4_workspace_bytes(int batch, int num_q_heads, int, int num_sms) {
+  return ws_layout(batch, 1, num_q_heads, num_sms).total;
+}
+
+cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
+  return launch_stream(a, 0, num_sms, stream);
+}
+
+bool rows_q4_fit(int max_seqlen_q, int num_q_heads, int num_kv_heads) {
+  return static_cast<int64_t>(max_seqlen_q) * ((num_q_heads + num_kv_heads - 1) / num_kv_heads) <= 32;
+}
+
+size_t rows_q4_workspace_bytes(int num_seqs, int max_seqlen_q, int num_q_heads, int num_sms) {
+  return ws_layout(num_seqs, max_seqlen_q, num_q_heads, num_sms).total;
+}
+
+cudaError_t launch_rows_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
+  return launch_stream(a, a.max_seqlen_q, num_sms, stream);
 }
 
 PKV_DEFINE_READ_ERROR(read_error_decode_q4, g_err_decode_q4)

@@ -166,9 +166,6 @@ struct Packed {
   uint2 s;     // 8 scales
 };
 
-// Bytes of w that are e4m3 NaNs, as 0xff.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
-
 // L2 prefetch of token `i`'s row of 128-token tile j (its codes and scales).
 __device__ __forceinline__ void prefetch_row(const Params& p, const int32_t* table, int j, bool is_v, int i, int g) {
   const int phys = __ldg(table + (j >> 1));
@@ -191,7 +188,7 @@ __device__ __forceinline__ void fetch(const Params& p, const int32_t* table, int
 #pragma unroll
   for (int u = 0; u < 4; ++u) o.d[u] = __ldg(d + u);
   const uint2 vs = __ldg(reinterpret_cast<const uint2*>(p.c.v_scales + row * q4::kRowScales));
-  const uint32_t n0 = nan_bytes(vs.x), n1 = nan_bytes(vs.y);
+  const uint32_t n0 = q4::nan_bytes(vs.x), n1 = q4::nan_bytes(vs.y);
   if (is_v) {
     const bool real = kTileN * j + i < len;
     o.s = make_uint2(real ? vs.x & ~n0 : 0u, real ? vs.y & ~n1 : 0u);
@@ -809,11 +806,15 @@ WsLayout ws_layout(const Plan& a, int num_seqs, int total_q, int hq) {
 
 size_t prefill_q4_workspace_bytes(int total_q, int num_seqs, int max_seqlen_q, int max_seqlen_k, int num_q_heads,
                                   int num_kv_heads, int num_sms) {
+  if (rows_q4_fit(max_seqlen_q, num_q_heads, num_kv_heads))
+    return rows_q4_workspace_bytes(num_seqs, max_seqlen_q, num_q_heads, num_sms);
   const Plan a = plan_for(num_seqs, max_seqlen_q, max_seqlen_k, num_q_heads, num_kv_heads, num_sms);
   return a.pieces ? ws_layout(a, num_seqs, total_q, num_q_heads).total : 256;
 }
 
 cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
+  // Few query rows a kv head: the streaming kernel.
+  if (rows_q4_fit(a.max_seqlen_q, a.num_q_heads, a.cache.num_kv_heads)) return launch_rows_q4(a, num_sms, stream);
   const Plan pl = plan_for(a.num_seqs, a.max_seqlen_q, a.max_seqlen_k, a.num_q_heads, a.cache.num_kv_heads, num_sms);
   void (*kernel)(CUtensorMap, Params) = pl.pieces ? prefill_q4_kernel<true> : prefill_q4_kernel<false>;
   // The warpgroups' requests for registers can only be met if the kernel was

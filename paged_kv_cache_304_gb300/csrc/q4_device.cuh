@@ -50,6 +50,9 @@ __device__ __forceinline__ uint32_t dec_scale2(uint32_t two) {
   return r;
 }
 
+// Bytes of w that are e4m3 NaNs, as 0xff.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
 __device__ __forceinline__ float half_lo(uint32_t h2) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xffffu)));
 }
