@@ -762,78 +762,91 @@ __global__ void __launch_bounds__(threads_of<NT>(), 1)
 }
 
 // Merge the partials of sequences that straddle CTAs; zero pad rows (one token a
-// sequence; with rows, what no valid sequence owns is left alone).  One warp per
-// query row and head, lane i dims 4i .. 4i+3; the lanes share the pass over the
-// partials' maxima and weights.
+// sequence; with rows, what no valid sequence owns is left alone).  Lane i of a
+// warp holds dims 4i .. 4i+3 and merges partials as it reads them, four in
+// flight.  Latency is all there is to it, so with few query rows (kWide) the four
+// warps of a CTA share a row's partials; otherwise each warp takes a row.
 constexpr int kCombineWarps = 4;
 
-template <bool kRows>
+template <bool kRows, bool kWide>
 __global__ void __launch_bounds__(32 * kCombineWarps) combine_q4_kernel(const Params p, int grid) {
+  __shared__ float s_ml[kCombineWarps][2];
+  __shared__ float4 s_o[kCombineWarps][32];
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t pair = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t pair = kWide ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kCombineWarps + warp;
   // row: of one token a sequence the sequence, else row `tok` of sequence blockIdx.y
   const int row = static_cast<int>(pair / p.Hq), hq = static_cast<int>(pair - static_cast<int64_t>(row) * p.Hq);
-  const int lane = threadIdx.x & 31;
   const int b = kRows ? blockIdx.y : row, tok = kRows ? row : 0;
   if (kRows ? tok >= p.max_q : b >= p.B) return;
-  int first = b;
-  if (kRows) {
-    first = __ldg(p.cu_q + b);
-    if (tok >= __ldg(p.cu_q + b + 1) - first) return;
-    first += tok;
-  }
-  const int L_in = length_of<kRows>(p, b);
-  const int2 meta = p.ws_meta[b];  // read only when the length is positive, i.e. when it was written
-  const int L = clamp_len(L_in, p.lmax);
-  if (kRows && L == 0) return;
+  const int2 meta = p.ws_meta[b];  // used only when the length is positive, i.e. when it was written
+  const int first = kRows ? __ldg(p.cu_q + b) + tok : b;
+  const int L = clamp_len(length_of<kRows>(p, b), p.lmax);
+  if (kRows && (L == 0 || first >= __ldg(p.cu_q + b + 1))) return;
   uint16_t* o = p.out + (static_cast<int64_t>(first) * p.Hq + hq) * kHeadDim + 4 * lane;
   if (L == 0) {
-    *reinterpret_cast<uint2*>(o) = make_uint2(0u, 0u);
+    if (!kWide || warp == 0) *reinterpret_cast<uint2*>(o) = make_uint2(0u, 0u);
     return;
   }
   const int c0 = max(0, meta.x), c1 = min(grid - 1, meta.y);
   if (c1 <= c0) return;  // finished inside one CTA
-  // The lanes share the pass over the maxima; then the weights come from the lane
-  // that holds a partial, with the outputs of eight partials in flight.
   const int64_t step = static_cast<int64_t>(p.max_q) * p.Hq;
   const int64_t at0 = (static_cast<int64_t>(b) * p.max_q + tok) * p.Hq + hq;
-  float top = -FLT_MAX;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, p.ws_ml[at0 + c * step].x);
-#pragma unroll
-  for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  float lsum = 0.f;
+  float M = -FLT_MAX, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int base = c0; base <= c1; base += 32) {
-    float w = 0.f;
-    if (base + lane <= c1) {
-      const float2 ml = p.ws_ml[at0 + (base + lane) * step];
-      w = fast_exp2(ml.x - top);
-      lsum += w * ml.y;
+  constexpr int kHop = kWide ? kCombineWarps : 1;
+  for (int c = c0 + (kWide ? warp : 0); c <= c1; c += 4 * kHop) {
+    float2 ml[4];
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = at0 + min(c + k * kHop, c1) * step;
+      ml[k] = p.ws_ml[at];
+      v[k] = *reinterpret_cast<const float4*>(p.ws_o + at * kHeadDim + 4 * lane);
     }
-    const int n = min(32, c1 - base + 1);
-    const float4* src = reinterpret_cast<const float4*>(p.ws_o + (at0 + base * step) * kHeadDim) + lane;
-    const int64_t hop = step * (kHeadDim / 4);
-    for (int i = 0; i < n; i += 8) {
-      float4 v[8];
+    float n = M;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        v[k] = i + k < n ? src[(i + k) * hop] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < 4; ++k) n = fmaxf(n, ml[k].x);
+    const float keep = fast_exp2(M - n);
+    M = n;
+    sum *= keep;
+    acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float x = __shfl_sync(0xffffffffu, w, (i + k) & 31);
-        if (i + k < n) {
-          acc.x += x * v[k].x;
-          acc.y += x * v[k].y;
-          acc.z += x * v[k].z;
-          acc.w += x * v[k].w;
-        }
-      }
+    for (int k = 0; k < 4; ++k) {
+      if (c + k * kHop > c1) break;
+      const float w = fast_exp2(ml[k].x - M);
+      sum += w * ml[k].y;
+      acc.x += w * v[k].x;
+      acc.y += w * v[k].y;
+      acc.z += w * v[k].z;
+      acc.w += w * v[k].w;
     }
   }
-#pragma unroll
-  for (int s = 16; s; s >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, s);
-  const float inv = p.v_scale / lsum;
+  if (kWide) {
+    if (lane == 0) {
+      s_ml[warp][0] = M;
+      s_ml[warp][1] = sum;
+    }
+    s_o[warp][lane] = acc;
+    __syncthreads();
+    if (warp) return;
+    float top = M;
+    for (int k = 1; k < kCombineWarps; ++k) top = fmaxf(top, s_ml[k][0]);
+    const float keep = fast_exp2(M - top);
+    sum *= keep;
+    acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+    for (int k = 1; k < kCombineWarps; ++k) {
+      const float w = fast_exp2(s_ml[k][0] - top);
+      const float4 v = s_o[k][lane];
+      sum += w * s_ml[k][1];
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    }
+  }
+  const float inv = p.v_scale / sum;
   *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
@@ -945,10 +958,12 @@ cudaError_t launch_stream(const AttnQ4Args& a, int max_q, int num_sms, cudaStrea
   const cudaError_t e = go(pl, p, km, vm, grid, stream);
   if (e != cudaSuccess) return e;
   const int64_t pairs = static_cast<int64_t>(max_q ? max_q : p.B) * p.Hq;
-  const unsigned x = static_cast<unsigned>((pairs + kCombineWarps - 1) / kCombineWarps);
-  if (max_q)
-    return launch_pdl(combine_q4_kernel<true>, dim3(x, p.B), dim3(32 * kCombineWarps), 0, stream, p, grid);
-  return launch_pdl(combine_q4_kernel<false>, dim3(x), dim3(32 * kCombineWarps), 0, stream, p, grid);
+  // A CTA a row while that makes at most eight CTAs an SM.
+  const bool wide = pairs * (max_q ? p.B : 1) <= 8 * static_cast<int64_t>(num_sms);
+  const unsigned x = static_cast<unsigned>(wide ? pairs : (pairs + kCombineWarps - 1) / kCombineWarps);
+  auto combine = max_q ? (wide ? combine_q4_kernel<true, true> : combine_q4_kernel<true, false>)
+                       : (wide ? combine_q4_kernel<false, true> : combine_q4_kernel<false, false>);
+  return launch_pdl(combine, dim3(x, max_q ? p.B : 1), dim3(32 * kCombineWarps), 0, stream, p, grid);
 }
 
 }  // namespace
