@@ -398,21 +398,24 @@ __device__ void consumer(const Params& p, const Smem& sm) {
       } else if (!mbar_wait(&sm.qfull[qs], (units / kQSlots) & 1u, &g_err_decode_q4)) {
         return;
       }
+      // Rows come from global memory, all requested together; a staged query is
+      // read twice (the largest element first) to keep few registers live.
+      uint4 raw[kRows ? NT : 1][4];
+      if (kRows) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int col = min(g + 8 * n, columns - 1), tok = col / p.G;
+          const uint4* row = reinterpret_cast<const uint4*>(
+                                 p.q + (static_cast<int64_t>(q0 + tok) * p.Hq + h * p.G + col - tok * p.G) * kHeadDim) + 4 * c;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) raw[kRows ? n : 0][i] = __ldg(row + i);
+        }
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        // Two passes over the 64 bytes (the largest element first) keep few registers live.
         const bool real = g + 8 * n < columns;
-        const int col = real ? g + 8 * n : 0;
-        uint32_t src = 0;
-        const uint4* row = nullptr;
-        if (kRows) {
-          const int tok = col / p.G;
-          row = reinterpret_cast<const uint4*>(
-                    p.q + (static_cast<int64_t>(q0 + tok) * p.Hq + h * p.G + col - tok * p.G) * kHeadDim) + 4 * c;
-        } else {
-          src = smem_u32(sm.qbuf) + qs * p.q_slot_bytes + (h * p.G + col) * (kHeadDim * 2) + c * 64;
-        }
-        auto load = [&](int i) { return kRows ? __ldg(row + i) : lds128(src + 16 * i); };
+        const uint32_t src = smem_u32(sm.qbuf) + qs * p.q_slot_bytes + (h * p.G + (real ? g + 8 * n : 0)) * (kHeadDim * 2) + c * 64;
+        auto load = [&](int i) { return kRows ? raw[kRows ? n : 0][i] : lds128(src + 16 * i); };
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -974,10 +977,6 @@ size_t decode_q4_workspace_bytes(int batch, int num_q_heads, int, int num_sms) {
 
 cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
   return launch_stream(a, 0, num_sms, stream);
-}
-
-bool rows_q4_fit(int max_seqlen_q, int num_q_heads, int num_kv_heads) {
-  return static_cast<int64_t>(max_seqlen_q) * ((num_q_heads + num_kv_heads - 1) / num_kv_heads) <= 32;
 }
 
 size_t rows_q4_workspace_bytes(int num_seqs, int max_seqlen_q, int num_q_heads, int num_sms) {

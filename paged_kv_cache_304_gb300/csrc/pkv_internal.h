@@ -214,9 +214,7 @@ size_t prefill_q4_workspace_bytes(int total_q, int num_seqs, int max_seqlen_q, i
 bool encode_q4_query_map(const uint16_t* q, int total_q, int num_q_heads, int log2_heads, CUtensorMap* m);
 cudaError_t launch_paged_attn_decode_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream);
-// Prefill of few rows by the decode kernel (decode_q4.cu): whether a step's rows
-// fit, its workspace, its launch.
-bool rows_q4_fit(int max_seqlen_q, int num_q_heads, int num_kv_heads);
+// Prefill of at most 32 rows a kv head by the decode kernel (decode_q4.cu).
 size_t rows_q4_workspace_bytes(int num_seqs, int max_seqlen_q, int num_q_heads, int num_sms);
 cudaError_t launch_rows_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream);
 

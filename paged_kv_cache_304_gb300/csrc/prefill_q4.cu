@@ -789,6 +789,17 @@ Plan plan_for(int num_seqs, int max_q, int max_k, int hq, int hkv, int num_sms) 
   return a;
 }
 
+// Few query rows a kv head go to the streaming kernel: up to 16 always, up to 32
+// when the tile kernel could not split the keys.  Measured (us, streaming / tile
+// kernel; 16 q, 8 kv heads): 4 sequences of 8192-32768 keys with 2, 8, 16 new
+// tokens 34 / 65, 45 / 72, 69 / 72; 4 of 600-1000 keys 12 / 15, -, 27 / 17;
+// 64 of 600-1000 keys 28 / 67, -, 57 / 64; 32 of 8192-32768 keys -, 199 / 561,
+// 386 / 640.
+bool use_rows(const Plan& a, int max_q, int hq, int hkv) {
+  const int64_t columns = static_cast<int64_t>(max_q) * ((hq + hkv - 1) / hkv);
+  return columns <= 16 || (columns <= 32 && !a.pieces);
+}
+
 struct WsLayout {
   size_t ml, pieces, total;
 };
@@ -806,16 +817,15 @@ WsLayout ws_layout(const Plan& a, int num_seqs, int total_q, int hq) {
 
 size_t prefill_q4_workspace_bytes(int total_q, int num_seqs, int max_seqlen_q, int max_seqlen_k, int num_q_heads,
                                   int num_kv_heads, int num_sms) {
-  if (rows_q4_fit(max_seqlen_q, num_q_heads, num_kv_heads))
-    return rows_q4_workspace_bytes(num_seqs, max_seqlen_q, num_q_heads, num_sms);
   const Plan a = plan_for(num_seqs, max_seqlen_q, max_seqlen_k, num_q_heads, num_kv_heads, num_sms);
+  if (use_rows(a, max_seqlen_q, num_q_heads, num_kv_heads))
+    return rows_q4_workspace_bytes(num_seqs, max_seqlen_q, num_q_heads, num_sms);
   return a.pieces ? ws_layout(a, num_seqs, total_q, num_q_heads).total : 256;
 }
 
 cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
-  // Few query rows a kv head: the streaming kernel.
-  if (rows_q4_fit(a.max_seqlen_q, a.num_q_heads, a.cache.num_kv_heads)) return launch_rows_q4(a, num_sms, stream);
   const Plan pl = plan_for(a.num_seqs, a.max_seqlen_q, a.max_seqlen_k, a.num_q_heads, a.cache.num_kv_heads, num_sms);
+  if (use_rows(pl, a.max_seqlen_q, a.num_q_heads, a.cache.num_kv_heads)) return launch_rows_q4(a, num_sms, stream);
   void (*kernel)(CUtensorMap, Params) = pl.pieces ? prefill_q4_kernel<true> : prefill_q4_kernel<false>;
   // The warpgroups' requests for registers can only be met if the kernel was
   // built with exactly the launch's share per thread.

@@ -180,6 +180,23 @@ def test_copy_flags_bad_pairs_and_does_the_others():
     pkv.copy_blocks(d, i32([]), i32([]))
 
 
+def test_captured_bookkeeping_replays():
+    """Fork and free from one graph leave the counts as they were, every time."""
+    tab, ln, ref = pool([300, 512, 10], 20, 3)
+    t, l, r, par = i32(tab), i32(ln), i32(ref), i32([0, 1, 2, 0])
+    out = pkv.fork_blocks(t, l, par, r)
+    pkv.free_blocks(out[0], out[1], r)
+    want = [x.clone() for x in out]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkv.fork_blocks(t, l, par, r, out=out)
+        pkv.free_blocks(out[0], out[1], r)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(r.cpu().numpy(), ref) and all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 def test_binding_refusals():
     tab, ln, ref = pool([300, 10], 8, 2)
     with pytest.raises(TypeError):

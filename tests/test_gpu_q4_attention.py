@@ -218,6 +218,142 @@ def test_prefill_last_row_equals_decode():
     assert (np.abs(d.double().cpu().numpy() - out[-1:].double().cpu().numpy()) <= 2 * tol).all()
 
 
+@pytest.mark.parametrize("rows,hq,hkv", [(1, 4, 2), (4, 4, 2), (8, 4, 2), (16, 4, 2), (9, 8, 1), (2, 16, 1), (40, 4, 2)])
+def test_prefill_few_rows_at_every_offset(rows, hq, hkv):
+    """A few new tokens whose causal limits fall at every place of a tile, block and piece."""
+    prompts = [(n, n - rows) for n in (rows, rows + 1, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300, 511, 640)
+               if n >= rows]
+    prefill_case(prompts, hq, hkv, seed=rows, tail=2)
+    prefill_case([(5000 + rows, 5000)], hq, hkv, seed=rows + 1)
+
+
+@pytest.mark.parametrize("new,cached", [(3, 300), (40, 300), (140, 0), (200, 900)])
+@pytest.mark.parametrize("kv", [0, 1])
+def test_prefill_nan_reaches_only_queries_that_see_it(new, cached, kv):
+    """A NaN held in K or V of one new token: earlier rows are exact, later ones are NaN."""
+    n = cached + new
+    at = cached + new // 2
+    p = Pool([n], 2, 5)
+    slot = int(p.tables[0, at // 256]) * 256 + at % 256
+    p.s[kv].view(-1, 2, 8)[slot, 0, 3] = 0x7F  # head 0, dims 48..63
+    q = queries(new, 4, 9)
+    out = pkv.paged_attn_prefill_q4(q.to(dev()), p.cache, i32([0, new]), i32([0, n]), i32(p.tables), SCALE, new, n)
+    ref, tol = q4_ref.attention(q.double(), p.held[0][0], p.held[0][1], SCALE, cached + 1)
+    before = new // 2
+    q4_ref.check(out[:before], ref[:before], tol[:before], "rows before the token")
+    assert torch.isnan(out[before:, :2, 48:64]).all()
+    q4_ref.check(out[before:, 2:], ref[before:, 2:], tol[before:, 2:], "the other kv head")
+
+
+def test_decode_nan_and_pads():
+    """A NaN in a visible V group reaches that group's dims; stale ones behind the end reach nothing."""
+    p = Pool([300, 40], 2, 5)
+    slot = int(p.tables[0, 1]) * 256 + 10
+    p.s[1].view(-1, 2, 8)[slot, 1, 0] = 0xFF
+    q = queries(2, 4, 9)
+    out = pkv.paged_attn_decode_q4(q.to(dev()), p.cache, i32([300, 40]), i32(p.tables), SCALE)
+    assert torch.isnan(out[0, 2:, :16]).all() and torch.isfinite(out[0, :2].float()).all()
+    assert torch.isfinite(out[1].float()).all()
+
+
+def test_infinite_and_nan_queries_stay_in_their_rows():
+    p = Pool([300, 300], 2, 5)
+    q = queries(2, 4, 9)
+    q[0, 1, 5] = float("inf")
+    q[0, 2, 7] = float("nan")
+    out = pkv.paged_attn_decode_q4(q.to(dev()), p.cache, i32([300, 300]), i32(p.tables), SCALE).float()
+    assert torch.isnan(out[0, 2]).all()
+    for b, h in ((0, 0), (0, 3), (1, 0), (1, 1), (1, 2), (1, 3)):
+        ref, tol = q4_ref.attention(q[b:b + 1].double().nan_to_num(posinf=0.0), p.held[b][0], p.held[b][1], SCALE, 300)
+        q4_ref.check(out[b:b + 1, h], ref[:, h], tol[:, h], f"row {b} head {h}")
+
+
+@pytest.mark.parametrize("kind", ["decode", "rows", "split", "tiles"])
+def test_captured_and_replayed_on_another_stream(kind):
+    """One captured call, replayed with changed inputs, equals the direct calls; two graphs keep their own workspaces."""
+    if kind == "decode":
+        lens, new = [700, 90, 2000], [1, 1, 1]
+    else:
+        lens = [700, 900, 2000]
+        new = {"rows": [3, 2, 4], "split": [30, 1, 40], "tiles": [700, 900, 2000]}[kind]
+    p = Pool(lens, 2, 11)
+    total = sum(new)
+    cu_q, cu_k = i32(np.concatenate([[0], np.cumsum(new)])), i32(np.concatenate([[0], np.cumsum(lens)]))
+    tab, ln = i32(p.tables), i32(lens)
+    q, outs = queries(total, 4, 1).to(dev()), [torch.zeros((total, 4, 128), dtype=torch.bfloat16, device=dev()) for _ in range(2)]
+
+    def call(out):
+        if kind == "decode":
+            return pkv.paged_attn_decode_q4(q, p.cache, ln, tab, SCALE, out=out)
+        return pkv.paged_attn_prefill_q4(q, p.cache, cu_q, cu_k, tab, SCALE, max(new), max(lens), out=out)
+
+    call(outs[0])
+    side = torch.cuda.Stream()
+    graphs = []
+    for o in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            call(o)
+        graphs.append(g)
+    for seed in (2, 3):
+        q.copy_(queries(total, 4, seed))
+        want = call(None)
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+    assert pkv.device_error() == []
+
+
+def test_two_calls_at_once_with_their_own_workspaces():
+    p = Pool([900, 3000, 20], 2, 12)
+    q = [queries(3, 4, s).to(dev()) for s in (1, 2)]
+    want = [pkv.paged_attn_decode_q4(x, p.cache, i32(p.lens), i32(p.tables), SCALE) for x in q]
+    ln, tab = i32(p.lens), i32(p.tables)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(pkv.paged_attn_decode_q4(q[i], p.cache, ln, tab, SCALE))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+def test_empty_batches():
+    p = Pool([30], 2, 7)
+    e = torch.empty((0, 4, 128), dtype=torch.bfloat16, device=dev())
+    t = torch.empty((0, 2), dtype=torch.int32, device=dev())
+    assert pkv.paged_attn_decode_q4(e, p.cache, i32([]), t, SCALE).shape == (0, 4, 128)
+    assert pkv.paged_attn_prefill_q4(e, p.cache, i32([0]), i32([0]), t, SCALE, 0, 0).shape == (0, 4, 128)
+
+
+def test_offsets_beyond_32_bits():
+    """Blocks whose codes lie more than 2^32 bytes into the cache."""
+    nb, hkv = 33000, 8  # 33000 * 256 * 8 * 64 bytes = 4.3 GB of codes each
+    c = pkv.Q4Cache.empty(nb, hkv, dev())
+    g = torch.Generator().manual_seed(1)
+    kv = torch.randn((2, 300, hkv, 128), generator=g).to(torch.bfloat16)
+    table = np.array([[nb - 1, nb - 2]], np.int32)
+    slots = np.array([table[0, t // 256] * 256 + t % 256 for t in range(300)], np.int32)
+    pkv.kv_cache_write_q4(kv[0].to(dev()), kv[1].to(dev()), i32(slots), c)
+    held = [q4_ref.values(*q4_ref.quantise(kv[i])) for i in range(2)]
+    back = pkv.kv_cache_read_q4(c, i32(slots))
+    for x, h in zip(back, held):
+        assert np.array_equal(x.double().cpu().numpy(), h)
+    q = queries(130, 16, 3)
+    ref, tol = q4_ref.attention(q.double(), held[0], held[1], SCALE, 171)
+    for rows in (slice(129, 130), slice(126, 130), slice(0, 130)):
+        n = rows.stop - rows.start
+        out = pkv.paged_attn_prefill_q4(q[rows].to(dev()), c, i32([0, n]), i32([0, 300]), i32(table), SCALE, n, 300)
+        q4_ref.check(out, ref[rows], tol[rows], f"{n} rows")
+    out = pkv.paged_attn_decode_q4(q[129:].to(dev()), c, i32([300]), i32(table), SCALE)
+    q4_ref.check(out, ref[129:], tol[129:], "decode")
+
+
 def test_binding_refusals():
     p = Pool([300], 2, 7)
     q = queries(1, 4, 3).to(dev())

@@ -1,0 +1,159 @@
+"""The new calls together, as an engine runs them: a prompt through norm + rotation
+into the 4-bit cache and prefill, sequences forked, a few decode steps of all
+children from a captured graph, the finished ones freed, the pool compacted, and
+decoding continued -- against one 64-bit model that keeps every sequence whole."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_304_gb300 as pkv
+from tests import q4_ref
+from tests.gpu_util import dev, i32
+
+pytestmark = pytest.mark.gpu
+HQ, HKV, EPS, BASE, SCALE = 8, 2, 1e-6, 1e4, 1 / math.sqrt(128)
+
+
+def project(n, seed):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn((n, HQ + 2 * HKV, 128), generator=g) * 2).to(torch.bfloat16)
+
+
+def rotate(x, w, pos):
+    """Norm + rotation in 64 bits, rounded to bf16 as the operator's definition says."""
+    x = x.double()
+    x = x / (x.square().mean(-1, keepdim=True) + EPS).sqrt() * w.double()
+    t = torch.as_tensor(pos).double()[:, None] * torch.tensor([BASE ** (-2.0 * i / 128) for i in range(64)]).double()
+    c, s = t.cos()[:, None], t.sin()[:, None]
+    a, b = x[..., :64], x[..., 64:]
+    return torch.cat((a * c - b * s, b * c + a * s), -1).to(torch.bfloat16)
+
+
+class Model:
+    """Sequences as lists of held K and V rows."""
+
+    def __init__(self, weights):
+        self.w, self.k, self.v = weights, [], []
+
+    def add(self, i, qkv, pos):
+        k = rotate(qkv[:, HQ:HQ + HKV], self.w[1], pos)
+        for store, x in ((self.k, k), (self.v, qkv[:, HQ + HKV:])):
+            store[i] = np.concatenate([store[i], q4_ref.values(*q4_ref.quantise(x))])
+
+
+def agree(out, q, k, v, first, what):
+    """Within the attention's allowance, plus what a differing rounding of q or of
+    one cached K row may move: a bf16 step in q (2^-7 relative) moves a score by
+    2^-7 |q k|; a K row rounded the other way before quantising may change codes.
+    Both are rare, so the median error is held to the allowance and every element
+    to the scores' bound with e = 2^-6 of the largest score."""
+    ref, tol = q4_ref.attention(q.double(), k, v, SCALE, first)
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert np.isfinite(err).all() and (np.median(err - tol) <= 0), what
+    big = float((q.double().abs().amax() * np.abs(k).max() * 128 * SCALE)) * 2.0**-6
+    assert (err <= tol + min(2.0, big) * np.abs(v).max()).all(), (what, float((err - tol).max()))
+    assert (err > tol).mean() < 0.02, (what, float((err > tol).mean()))
+
+
+def test_serving_steps():
+    nb, maxb = 24, 5
+    g = torch.Generator().manual_seed(0)
+    weights = [(1 + 0.2 * torch.randn(128, generator=g)).to(torch.bfloat16) for _ in range(2)]
+    wd = [w.to(dev()) for w in weights]
+    freqs = pkv.rope_frequencies(128, BASE, dev())
+    data = torch.zeros((2, nb, 256, HKV, 64), dtype=torch.uint8, device=dev())
+    scales = torch.full((2, nb, 256, HKV, 8), 0x7F, dtype=torch.uint8, device=dev())  # stale NaN everywhere
+    cache = pkv.Q4Cache(data[0], scales[0], data[1], scales[1])
+    model = Model(weights)
+
+    # prompts of 300 and 512 tokens in one step
+    lens = [300, 512]
+    tables = np.full((2, maxb), -1, np.int32)
+    tables[0, :2], tables[1, :2] = [20, 3], [11, 22]
+    ref = np.zeros(nb, np.int32)
+    ref[[20, 3, 11, 22]] = 1
+    qkv = project(sum(lens), 1)
+    pos = np.concatenate([np.arange(n) for n in lens])
+    slots = np.concatenate([tables[i][np.arange(n) // 256] * 256 + np.arange(n) % 256 for i, n in enumerate(lens)])
+    d = qkv.to(dev())
+    q = pkv.qk_norm_rope_write_q4(d[:, :HQ], d[:, HQ:HQ + HKV], d[:, HQ + HKV:], *wd, EPS, freqs, i32(pos), i32(slots),
+                                  cache)
+    cu = i32([0, 300, 812])
+    out = pkv.paged_attn_prefill_q4(q, cache, cu, cu, i32(tables), SCALE, 512, 512)
+    for i, at in enumerate((0, 300)):
+        rows = slice(at, at + lens[i])
+        model.k.append(np.zeros((0, HKV, 128)))
+        model.v.append(np.zeros((0, HKV, 128)))
+        model.add(i, qkv[rows], pos[rows])
+        agree(out[rows], rotate(qkv[rows, :HQ], weights[0], pos[rows]), model.k[i], model.v[i], 1, f"prompt {i}")
+
+    # three children of the first, one of the second
+    d_ref, parents = i32(ref), [0, 0, 1, 0]
+    ct, cl, src, dst = pkv.fork_blocks(i32(tables), i32(lens), i32(parents), d_ref)
+    for x in (data, scales):
+        pkv.copy_blocks(x, src, dst, block_dim=1)
+    assert [int(x) for x in d_ref[[20, 3, 11, 22]]] == [4, 1, 2, 2]  # the prompts still hold theirs
+    pkv.free_blocks(i32(tables), i32(lens), d_ref)
+    model.k, model.v = ([x[p].copy() for p in parents] for x in (model.k, model.v))
+    tab, ln, n = ct.cpu().numpy(), [300, 300, 512, 300], 4
+    held = d_ref.cpu().numpy()
+
+    # a captured decode step, replayed with every step's inputs
+    st = {"qkv": torch.zeros((n, HQ + 2 * HKV, 128), dtype=torch.bfloat16, device=dev()), "pos": i32([0] * n),
+          "slots": i32([-1] * n), "lens": i32([0] * n), "tab": i32(tab)}
+    out = torch.zeros((n, HQ, 128), dtype=torch.bfloat16, device=dev())
+    ws = pkv.decode_q4_workspace(n, HQ, HKV, dev())
+
+    def step():
+        x = st["qkv"]
+        q = pkv.qk_norm_rope_write_q4(x[:, :HQ], x[:, HQ:HQ + HKV], x[:, HQ + HKV:], *wd, EPS, freqs, st["pos"],
+                                      st["slots"], cache)
+        pkv.paged_attn_decode_q4(q, cache, st["lens"], st["tab"], SCALE, out=out, workspace=ws)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+
+    def decode(seed, rows):
+        x = project(n, seed)
+        slots, pos, lens = [-1] * n, [0] * n, [0] * n  # pad rows by default
+        for i in rows:
+            p = ln[i]
+            if p % 256 == 0:  # opens a block
+                tab[i, p // 256] = int(np.nonzero(held == 0)[0][0])
+                held[tab[i, p // 256]] = 1
+            slots[i], pos[i], lens[i] = tab[i, p // 256] * 256 + p % 256, p, p + 1
+            ln[i] = p + 1
+            model.add(i, x[i:i + 1], [p])
+        for name, v in (("qkv", x.to(dev())), ("pos", i32(pos)), ("slots", i32(slots)), ("lens", i32(lens)), ("tab", i32(tab))):
+            st[name].copy_(v)
+        graph.replay()
+        for i in range(n):
+            if i in rows:
+                agree(out[i:i + 1], rotate(x[i:i + 1, :HQ], weights[0], [ln[i] - 1]), model.k[i], model.v[i], ln[i],
+                      f"step {seed}, sequence {i}")
+            else:
+                assert (out[i] == 0).all()
+
+    for seed in (10, 11, 12):
+        decode(seed, range(n))
+
+    # two sequences end, their blocks are given back and the pool is compacted
+    d_ref = i32(held)
+    pkv.free_blocks(i32(tab[[0, 2]]), i32([ln[0], ln[2]]), d_ref)
+    keep = [1, 3]
+    new_tab, new_ref, src, dst, moves = pkv.compact_blocks(i32(tab[keep]), i32([ln[i] for i in keep]), d_ref)
+    for x in (data, scales):
+        pkv.copy_blocks(x, src, dst, block_dim=1)
+    live = int((new_ref > 0).sum())
+    assert (new_ref[:live] > 0).all() and (new_ref[live:] == 0).all() and int(moves) > 0
+    # whatever the freed blocks hold now must not matter
+    data[:, live:], scales[:, live:] = 0x77, 0x7F
+    tab[keep], held = new_tab.cpu().numpy(), new_ref.cpu().numpy()
+    for seed in (20, 21):
+        decode(seed, keep)
+    assert pkv.device_error() == []
