@@ -6,19 +6,19 @@
 // codes into matrix operands has to fit into a quarter of the time that the
 // bf16 kernel has.
 //
-// * Work split.  The sequences' tiles of T = 32 R tokens are laid end to end and
-//   every CTA takes an equal share of the tiles (persistent CTAs, one to three
-//   per SM).  Sequences that straddle CTAs leave partial (max, sum, output)
-//   triples that a combine kernel merges.
+// * Work split.  The sequences' stages of 32 tokens are laid end to end and every
+//   CTA (one per SM) takes an equal share of them.  Sequences that straddle CTAs
+//   leave partial (max, sum, output) triples that a combine kernel merges.
 // * Pipeline.  A producer warp fetches a tile's K and V codes for all kv heads
 //   with one TMA tensor copy each, laid out [head][token][64 bytes] with the
 //   64-byte swizzle, and the scales, which are contiguous, with plain bulk copies
 //   into a ring of 32-token stages.
-// * Operands.  Warp (h, r) computes kv head h for tokens 32r .. 32r+31 of a
-//   tile in two interleaved steps of 16.  The tokens are the rows of S^T = K Q^T (m16n8k16, fp16 in, fp32
-//   out; the group's query heads are the 8 columns) and then the inner dimension
-//   of O^T = V^T P^T, so a group of up to 8 query heads wastes no matrix work on
-//   empty rows.  The order of dims in the first product and of tokens in the
+// * Operands.  Warp (h, r) of a kv head's R warps takes every R-th stage, in two
+//   interleaved steps of 16 tokens; the R results are merged when the CTA's part
+//   of a sequence ends.  The tokens are the rows of S^T = K Q^T (m16n8k16, fp16 in,
+//   fp32 out; the group's query heads are the 8 columns) and then the inner
+//   dimension of O^T = V^T P^T, so a group of up to 8 query heads wastes no matrix
+//   work on empty rows.  The order of dims in the first product and of tokens in the
 //   second is free as long as both operands agree:
 //     - a lane takes 32 consecutive dims of its two K rows (one 16-byte load,
 //       two scales a row) and the same 32 dims of its query head;
@@ -110,7 +110,7 @@ struct Params {
   float2* ws_ml;  // [slots, max_q, Hq] (row max in log2 units, row sum)
   int2* ws_meta;  // [B] first and last CTA holding sequence b
   int32_t maxb, B, Hq, Hkv, G, num_blocks, lmax;
-  int32_t log2_r, log2_tile, stages;  // R, T and the ring's depth
+  int32_t log2_r, stages;  // R and the ring's depth
   float sl2;      // scale * k_scale * log2(e)
   float v_scale;
   uint32_t data_bytes, scale_bytes, stage_bytes, q_slot_bytes, q_bytes;
@@ -194,13 +194,13 @@ __device__ __forceinline__ int load_block(const Params& p, int b, int lb) {
   return phys;
 }
 
-// Issue every tile of unit (b, [lo, hi)), lo a multiple of the tile: R stages of
-// 32 tokens each.  Lane 0 of the producer warp only.
+// Issue every stage of unit (b, [lo, hi)), lo a multiple of 32, and empty ones up
+// to a multiple of R stages.  Lane 0 of the producer warp only.
 template <bool kRows>
 __device__ void emit_unit(const Params& p, const Smem& sm, const CUtensorMap* kmap, const CUtensorMap* vmap,
                           ProducerState& ps, int b, int lo, int hi, int L, int first_phys) {
   int lb_cur = -1, phys = 0, nxt = first_phys;
-  const int tile = 1 << p.log2_tile;
+  const int tile = kStepTokens << p.log2_r;
   const int end = lo + ((hi - lo + tile - 1) & ~(tile - 1));
   for (int t = lo; t < end; t += kStepTokens) {
     const uint32_t st = ps.stage;
@@ -270,7 +270,6 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
   }
   // Lengths are loaded 256 at a time, all loads together; a batch of at most
   // 256 sequences is loaded once for both passes.
-  const int round = (1 << p.log2_tile) - 1;
   int len[8];
   auto load_lengths = [&](int base) {
 #pragma unroll
@@ -278,18 +277,31 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
 #pragma unroll
     for (int i = 0; i < 8; ++i) len[i] = clamp_len(len[i], p.lmax);
   };
-  long long total = 0;  // tiles of the batch
+  // The share of a CTA is counted in stages, or, where the batch is so small that
+  // one round of R stages a CTA holds it, in such rounds: then no CTA has parts of
+  // two sequences (4 sequences of 1 to 600 tokens, 8 kv heads: 10.1 us against
+  // 12.8; 256 of 100 to 2048 tokens, in rounds 71.4 us against 69.9).
+  long long total = 0, rounds = 0;
   for (int base = 0; base < p.B; base += 256) {
     load_lengths(base);
-    unsigned n = 0;
+    unsigned n = 0, m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) n += static_cast<unsigned>((len[i] + round) >> p.log2_tile);
+    for (int i = 0; i < 8; ++i) {
+      const int k = (len[i] + kStepTokens - 1) / kStepTokens;
+      n += static_cast<unsigned>(k);
+      m += static_cast<unsigned>((k + (1 << p.log2_r) - 1) >> p.log2_r);
+    }
     total += __reduce_add_sync(0xffffffffu, n);
+    rounds += __reduce_add_sync(0xffffffffu, m);
   }
+  const bool in_rounds = rounds <= gridDim.x;
+  const int log2_tile = 5 + (in_rounds ? p.log2_r : 0);
+  const int up = (1 << log2_tile) - 1;
+  if (in_rounds) total = rounds;
   ProducerState ps;
   if (total > 0) {
     long long per = (total + gridDim.x - 1) / gridDim.x;
-    const int least = max(1, kMinTokens >> p.log2_tile);
+    const int least = max(1, kMinTokens >> log2_tile);
     if (per < least) per = least;
     const long long my_lo = static_cast<long long>(blockIdx.x) * per;
     const long long my_hi = my_lo + per < total ? my_lo + per : total;
@@ -300,7 +312,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
       int L = len[0];
 #pragma unroll
       for (int i = 0; i < 7; ++i) len[i] = len[i + 1];
-      const int n = (L + round) >> p.log2_tile;
+      const int n = (L + up) >> log2_tile;
       const int incl = warp_incl_scan(n, lane);
       const long long Sb = S + incl - n;
       if (n > 0 && Sb / per == blockIdx.x)
@@ -309,8 +321,8 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
       const long long hi = my_hi < Sb + n ? my_hi : Sb + n;
       const bool has = n > 0 && lo < hi;
       unsigned mask = __ballot_sync(0xffffffffu, has);
-      const int lo_t = has ? static_cast<int>(lo - Sb) << p.log2_tile : 0;
-      const int hi_t = has ? min(L, static_cast<int>(hi - Sb) << p.log2_tile) : 0;
+      const int lo_t = has ? static_cast<int>(lo - Sb) << log2_tile : 0;
+      const int hi_t = has ? min(L, static_cast<int>(hi - Sb) << log2_tile) : 0;
       const int first_phys = has ? load_block(p, b, lo_t / kBlockSize) : 0;  // of every piece together
       while (mask) {
         const int j = __ffs(mask) - 1;
@@ -947,7 +959,6 @@ cudaError_t launch_stream(const AttnQ4Args& a, int max_q, int num_sms, cudaStrea
   p.num_blocks = a.cache.num_blocks;
   p.lmax = static_cast<int>(std::min<long long>(a.max_seqlen_k, static_cast<long long>(p.maxb) * kBlockSize));
   p.log2_r = pl.log2_r;
-  p.log2_tile = pl.log2_r + 5;  // tiles of 32 R tokens
   p.stages = pl.stages;
   p.sl2 = a.scale * a.cache.k_scale * 1.4426950408889634f;
   p.v_scale = a.cache.v_scale;
