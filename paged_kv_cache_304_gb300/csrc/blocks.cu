@@ -197,8 +197,22 @@ __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const Compac
   if (threadIdx.x == 0) *p.num_moves = movers;
 }
 
-// Entries of blocks that moved follow them: binary search in the ascending list
-// of movers.
+// Place of x in an ascending list of n, or -1.
+__device__ __forceinline__ int find(const int32_t* list, int n, int x) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (list[mid] < x)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo < n && list[lo] == x ? lo : -1;
+}
+
+// Entries of blocks that moved follow them.  With the moves done the blocks below
+// the live count are held and no others, so a block was held if it is one of the
+// movers, or is held now and was not a hole.
 __global__ void __launch_bounds__(256) compact_tables_kernel(const CompactArgs p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -214,19 +228,14 @@ __global__ void __launch_bounds__(256) compact_tables_kernel(const CompactArgs p
     } else if (j < blocks_of(len)) {
       if (b < 0 || b >= p.num_blocks) {
         atomicOr(&g_err_blocks, PKV_DEVERR_BLOCK_RANGE);
-      } else if (moves > 0 && b >= p.copy_src[0]) {
-        int lo = 0, hi = moves - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (p.copy_src[mid] < b)
-            lo = mid + 1;
-          else
-            hi = mid;
-        }
-        if (p.copy_src[lo] == b)
-          b = p.copy_dst[lo];
+      } else if (p.new_ref_count[b] == 0) {
+        const int m = find(p.copy_src, moves, b);
+        if (m >= 0)
+          b = p.copy_dst[m];
         else
-          atomicOr(&g_err_blocks, PKV_DEVERR_BLOCK_RANGE);  // a block that nothing holds
+          atomicOr(&g_err_blocks, PKV_DEVERR_BLOCK_RANGE);
+      } else if (find(p.copy_dst, moves, b) >= 0) {
+        atomicOr(&g_err_blocks, PKV_DEVERR_BLOCK_RANGE);
       }
     }
     p.new_tables[e] = b;

@@ -153,6 +153,20 @@ def test_compact_flags_bad_rows():
     assert got[0][0, 0] == 77 and np.array_equal(got[0][1].cpu().numpy(), tab2[1])
 
 
+@pytest.mark.parametrize("entry", [0, 1, 3, 4, 15])
+def test_compact_flags_blocks_that_nothing_holds(entry):
+    """Held: 2, 9 and (but for entry 3) 3 of 16 blocks, so holes are 0 and 1 and what lies behind the live moves."""
+    ref = np.zeros(16, np.int32)
+    ref[[2, 9]] = 1
+    if entry != 3:
+        ref[3] = 1
+    tab = np.array([[2, 9], [entry, -1]], np.int32)
+    pkv.device_error(clear=True)
+    got = pkv.compact_blocks(i32(tab), i32([400, 10]), i32(ref))
+    assert pkv.device_error() == ["BLOCK_RANGE"]
+    assert got[0][0].tolist() == compact_ref(tab[:1], [400], ref)[0][0].tolist() and got[0][1].tolist() == [entry, -1]
+
+
 @pytest.mark.parametrize("shape,block_dim,dtype", [
     ((9, 256, 2, 128), 0, torch.bfloat16), ((2, 3, 9, 256, 1, 64), 2, torch.uint8), ((4, 9, 16), 1, torch.uint8),
     ((9, 5, 16), 0, torch.int32), ((2, 9, 65, 40), 1, torch.float32)])
