@@ -243,7 +243,10 @@ __global__ void __launch_bounds__(256) compact_tables_kernel(const CompactArgs p
 }
 
 // One CTA moves one 32 KiB piece at a time; each thread has eight 16-byte loads
-// in flight before its stores.
+// in flight before its stores.  The same piece of all copies comes before the next
+// piece, so that a block copied to several children is read from HBM once (24
+// children of 16 parents, 28 layers, 1.03 GB: 177.5 us, 5.8 TB/s; copy by copy
+// 214 us.  160 moves in 4 layers, 1.34 GB: 214 us, 6.27 TB/s).
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;
 constexpr int64_t kPieceVecs = static_cast<int64_t>(kCopyThreads) * kCopyUnroll;
@@ -254,11 +257,10 @@ __global__ void __launch_bounds__(kCopyThreads)
   griddep_wait();
   griddep_launch_dependents();
   const int64_t pieces = (block_vecs + kPieceVecs - 1) / kPieceVecs;
-  const int64_t per_copy = pieces * num_planes;
-  const int64_t items = per_copy * num_copies;
+  const int64_t items = pieces * num_planes * num_copies;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int i = static_cast<int>(it / per_copy);
-    const int64_t rest = it - i * per_copy;
+    const int64_t rest = it / num_copies;
+    const int i = static_cast<int>(it - rest * num_copies);
     const int64_t plane = rest / pieces, piece = rest - plane * pieces;
     const int from = __ldg(src + i), to = __ldg(dst + i);
     if (from < 0 || to < 0 || from >= num_blocks || to >= num_blocks) {
