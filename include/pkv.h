@@ -419,7 +419,9 @@ PKV_API pkv_status pkv_kv_cache_read_q4(const pkv_q4_cache* cache, const int32_t
  * (any bytes).  The values and the probabilities enter the products in fp16:
  * code * s is exact there, and a query row is scaled by a power of two so that
  * its largest element is in range, which loses nothing of elements down to
- * 2^-29 of it.  Accumulation is fp32.
+ * 2^-29 of it.  Accumulation is fp32.  A group of 16 that reads as NaN makes the
+ * scores (K) or its 16 dims of the output (V) NaN for the queries that see its
+ * token.
  */
 PKV_API size_t pkv_decode_q4_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads);
 PKV_API pkv_status pkv_paged_attn_decode_q4(const pkv_bf16* q, const pkv_q4_cache* cache,
@@ -430,7 +432,8 @@ PKV_API pkv_status pkv_paged_attn_decode_q4(const pkv_bf16* q, const pkv_q4_cach
 
 /*
  * Varlen causal prefill over the 4-bit cache: pkv_paged_attn_prefill with K and
- * V the values the cache holds; rounding as in pkv_paged_attn_decode_q4.
+ * V the values the cache holds; rounding as in pkv_paged_attn_decode_q4.  A V
+ * group that reads as NaN makes all 128 dims of the rows that see its token NaN.
  *   max_seqlen_q, max_seqlen_k  upper bounds of n_i and L_i.  A sequence beyond
  *                 them, with c_i < 0 or with L_i > max_blocks_per_seq *
  *                 block_size flags PKV_DEVERR_LEN_RANGE and its rows are not
@@ -438,9 +441,12 @@ PKV_API pkv_status pkv_paged_attn_decode_q4(const pkv_bf16* q, const pkv_q4_cach
  *   workspace     >= pkv_prefill_q4_workspace_bytes(total_q, num_seqs,
  *                 max_seqlen_q, max_seqlen_k, num_q_heads, num_kv_heads) device
  *                 bytes, 256-byte aligned, need not be initialised.  When the
- *                 query tiles are too few to occupy the GPU, the keys are split
+ *                 query rows are too few to occupy the GPU, the keys are split
  *                 over several CTAs and the pieces joined from there.  The size
  *                 depends on the current device's SM count.
+ * A few new tokens per sequence (max_seqlen_q times the query heads of a kv head
+ * up to 16, or 32 with many sequences) take the path of decode, with each row's
+ * causal limit.
  */
 PKV_API size_t pkv_prefill_q4_workspace_bytes(int32_t total_q, int32_t num_seqs, int32_t max_seqlen_q,
                                               int32_t max_seqlen_k, int32_t num_q_heads, int32_t num_kv_heads);
