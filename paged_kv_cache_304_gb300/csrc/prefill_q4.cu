@@ -15,12 +15,13 @@
 //   place, thread r its row r, scaled by a power of two so that the row's largest
 //   element is in [2^14, 2^15); then the softmax, thread r on row r (TMEM lane
 //   r), with the power of two undone in the row's softmax scale.
-// * warps 12-15 (with one slot only, warps 8-11 take the V tiles): thread i turns token i of the 128-token K and V tiles into fp16:
-//   64 bytes of codes and 8 scales, fetched into registers one step ahead (with one
-//   slot, where the loads' latency shows, also prefetched into L2 six steps ahead;
-//   with two, whose K/V tiles other CTAs read as well, that cost 14 %), become
-//   128 dims (one conversion and one multiplication per two dims, exact) written
-//   in the 128-byte swizzle that the matrix descriptors expect.
+// * warps 12-15 (with one slot only, warps 8-11 take the V tiles): thread i turns
+//   token i of the 128-token K and V tiles into fp16: 64 bytes of codes and 8
+//   scales, fetched into registers one step ahead (with one slot, where the loads'
+//   latency shows, also prefetched into L2 six steps ahead; with two, whose K/V
+//   tiles other CTAs read as well, that cost 14 %), become 128 dims (one conversion
+//   and one multiplication per two dims, exact) written in the 128-byte swizzle
+//   that the matrix descriptors expect.
 // Tensor memory: S (128 columns, handed from slot to slot), P_A | P_B (64 each,
 // packed fp16), O_A | O_B (128 each); the slots ping-pong so that one slot's
 // products run while the other's softmax does.
@@ -33,6 +34,10 @@
 // which ceil(tiles / C) pieces of every query tile need no more CTAs than there
 // are, and takes its piece.  Pieces leave (max, sum, unnormalised output) triples
 // for a combine kernel.
+// Measured: two prompts of 8192 tokens, 32 q and 8 kv heads, 820 us, 1335 TFLOP/s
+// (69 % of the bf16 burst rate; without the expansion's arithmetic no faster); 16384
+// new tokens of ragged prompts of 100 to 1024, 16 q and 8 kv heads, 105 us, of which
+// each query tile's start and end are half.
 // Every wait is bounded (two seconds); on timeout the CTA flags
 // PKV_DEVERR_WAIT_TIMEOUT, lets the copies and MMAs it has already issued
 // complete, frees its tensor memory and returns.
