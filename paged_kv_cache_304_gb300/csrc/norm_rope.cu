@@ -65,18 +65,138 @@ __device__ __forceinline__ void read8(const float* p, float2* x) {
 
 // kDest: 0 = k_out, 1 = bf16 cache (K and V), 2 = 4-bit cache (K and V).
 // kInter: rotated pairs are (2i, 2i + 1).
+enum Kind { kQ, kK, kV };
+
+struct Shared {
+  __align__(16) float cos[kMaxTokens][kPairs], sin[kMaxTokens][kPairs];
+  __align__(16) float weight[2][kHeadDim];
+  int slot[kMaxTokens];
+};
+
+// Four heads, group `group` of one kind, of tokens [t_begin, t_end) from t0 on; c0
+// and c1 are the lane's chunks.  (A function per kind: with the kind a variable
+// every token paid for its branches.)
+template <int kDest, bool kInter, Kind kKind>
+__device__ __forceinline__ void run_group(const NormRopeArgs& p, const Shared& sh, int64_t t0, int t_begin, int t_end,
+                                          int group, int c0, int c1) {
+  const int lane = threadIdx.x & 31, l = lane & 7;
+  const int head = 4 * group + (lane >> 3);
+  constexpr bool is_q = kKind == kQ, is_v = kKind == kV, to_cache = kDest != 0 && !is_q;
+  const bool real = head < (is_q ? p.num_q_heads : p.num_kv_heads);
+  // Steps and places in 16-byte chunks; plain loads: the output may be the input.
+  const int64_t step = (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) >> 3;
+  const uint4* src = reinterpret_cast<const uint4*>(is_q ? p.q : is_v ? p.v : p.k) + (t0 + t_begin) * step + head * kChunks;
+  const int64_t out_step = (is_q ? p.q_out_stride : p.k_out_stride) >> 3;
+  uint4* out = reinterpret_cast<uint4*>(is_q ? p.q_out : p.k_out) + (t0 + t_begin) * out_step + head * kChunks;
+  const bool norm = (is_q ? p.q_weight : p.k_weight) != nullptr;
+  const float* weight = sh.weight[is_q ? 0 : 1];
+  // row 0 of this lane's head in the cache (kDest 1: 16-byte chunks; 2: bytes)
+  uint4* rows16 = reinterpret_cast<uint4*>(is_v ? p.v_cache : p.k_cache) + head * kChunks;
+  uint8_t* data = (is_v ? p.q4.v_data : p.q4.k_data) + head * q4::kRowBytes;
+  uint8_t* scales = (is_v ? p.q4.v_scales : p.q4.k_scales) + head * q4::kRowScales;
+  const float inv = is_v ? p.q4.v_inv : p.q4.k_inv;
+  uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
+  if (real) {
+    n0 = src[c0];
+    n1 = src[c1];
+  }
+  for (int t = t_begin; t < t_end; ++t) {
+    uint4 a0 = n0, a1 = n1;
+    src += step;
+    if (real && t + 1 < t_end) {
+      n0 = src[c0];
+      n1 = src[c1];
+    }
+    if (!is_v) {
+      float2 x[8];
+      q4::unpack8(a0, x);
+      q4::unpack8(a1, x + 4);
+      if (norm) {
+        float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = ffma2(x[i], x[i], ss);
+        float sum = ss.x + ss.y;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        const float2 r = both(rsqrtf(sum * (1.f / kHeadDim) + p.eps));
+        float2 w[4];
+        read8(weight + 8 * c0, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fmul2(fmul2(x[i], r), w[i]);
+        read8(weight + 8 * c1, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i + 4] = fmul2(fmul2(x[i + 4], r), w[i]);
+      }
+      // The lane's pairs: elements of chunk c0 with those of c1 (halves), or
+      // neighbours within each chunk (interleaved: pairs 4 c0 .., 4 c1 ..).
+      float2 c[4], s[4];
+      if (kInter) {
+        read4(&sh.cos[t][4 * c0], c);
+        read4(&sh.cos[t][4 * c1], c + 2);
+        read4(&sh.sin[t][4 * c0], s);
+        read4(&sh.sin[t][4 * c1], s + 2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float ce = e & 1 ? c[e >> 1].y : c[e >> 1].x, se = e & 1 ? s[e >> 1].y : s[e >> 1].x;
+          const float2 z = x[e];
+          x[e] = make_float2(fmaf(-z.y, se, z.x * ce), fmaf(z.x, se, z.y * ce));
+        }
+      } else {
+        read8(&sh.cos[t][8 * l], c);
+        read8(&sh.sin[t][8 * l], s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = x[e], z = x[e + 4];
+          x[e] = ffma2(z, make_float2(-s[e].x, -s[e].y), fmul2(v, c[e]));
+          x[e + 4] = ffma2(v, s[e], fmul2(z, c[e]));
+        }
+      }
+      a0 = pack8(x);
+      a1 = pack8(x + 4);
+    }
+    if (!to_cache) {
+      if (real) {
+        out[c0] = a0;
+        out[c1] = a1;
+      }
+      out += out_step;
+    } else if (const int slot = sh.slot[t]; slot >= 0) {  // the whole warp
+      const int64_t row = static_cast<int64_t>(slot) * p.num_kv_heads;
+      if (kDest == 1) {
+        if (real) {
+          uint4* dst = rows16 + row * kChunks;
+          dst[c0] = a0;
+          dst[c1] = a1;
+        }
+      } else {
+        uint32_t b0, b1;
+        const uint32_t w0 = q4::quantise_chunk(a0, inv, &b0), w1 = q4::quantise_chunk(a1, inv, &b1);
+        if (real) {
+          uint32_t* d = reinterpret_cast<uint32_t*>(data + row * q4::kRowBytes);
+          d[c0] = w0;
+          d[c1] = w1;
+          if (!(lane & 1)) {  // even chunks: the scale of a group of two
+            uint8_t* sc = scales + row * q4::kRowScales;
+            sc[c0 >> 1] = static_cast<uint8_t>(b0);
+            sc[c1 >> 1] = static_cast<uint8_t>(b1);
+          }
+        }
+      }
+    }
+  }
+}
+
 template <int kDest, bool kInter>
 __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRopeArgs p, int tokens) {
-  __shared__ __align__(16) float s_cos[kMaxTokens][kPairs], s_sin[kMaxTokens][kPairs];
-  __shared__ __align__(16) float s_weight[2][kHeadDim];
-  __shared__ int s_slot[kMaxTokens];
+  __shared__ Shared sh;
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
   const int n = static_cast<int>(min(static_cast<int64_t>(tokens), p.num_tokens - t0));
 
-  const int l = lane & 7, sub = lane >> 3;
+  const int l = lane & 7;
   const int half_chunks = p.rope_dim >> 4;  // chunks in half of the rotated dims
   // The lane's chunks of 8 dims.  Rotated halves: chunk j and its partner
   // j + rope_dim/16 share a lane, the dims behind rope_dim fill the other
@@ -118,13 +238,13 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
         s = -s;
       }
     }
-    s_cos[tok][pair] = c;
-    s_sin[tok][pair] = s;
+    sh.cos[tok][pair] = c;
+    sh.sin[tok][pair] = s;
   }
   {
     const uint16_t* w = threadIdx.x < kHeadDim ? p.q_weight : p.k_weight;
     const int d = threadIdx.x % kHeadDim;
-    s_weight[threadIdx.x / kHeadDim][d] = w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + d)) << 16) : 1.f;
+    sh.weight[threadIdx.x / kHeadDim][d] = w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + d)) << 16) : 1.f;
   }
   if (kDest && threadIdx.x < n) {
     int s = __ldg(p.slots + t0 + threadIdx.x);
@@ -132,7 +252,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
       atomicOr(&g_err_norm_rope, PKV_DEVERR_SLOT_RANGE);
       s = -1;
     }
-    s_slot[threadIdx.x] = s;
+    sh.slot[threadIdx.x] = s;
   }
   __syncthreads();
 
@@ -144,112 +264,12 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
     const int g = u / n, t_begin = u - g * n;
     const int t_end = min(n, t_begin + u_end - u);
     u += t_end - t_begin;
-    const bool is_q = g < q_groups, is_v = g >= rope_groups;
-    const int head = 4 * (is_q ? g : is_v ? g - rope_groups : g - q_groups) + sub;
-    const bool real = head < (is_q ? p.num_q_heads : p.num_kv_heads);
-    // Steps and places in 16-byte chunks; plain loads: the output may be the input.
-    const int64_t step = (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) >> 3;
-    const uint4* src = reinterpret_cast<const uint4*>(is_q ? p.q : is_v ? p.v : p.k) + (t0 + t_begin) * step + head * kChunks;
-    const int64_t out_step = (is_q ? p.q_out_stride : p.k_out_stride) >> 3;
-    uint4* out = reinterpret_cast<uint4*>(is_q ? p.q_out : p.k_out) + (t0 + t_begin) * out_step + head * kChunks;
-    const bool norm = (is_q ? p.q_weight : p.k_weight) != nullptr;
-    const float* weight = s_weight[is_q ? 0 : 1];
-    const bool to_cache = kDest != 0 && !is_q;
-    // row 0 of this lane's head in the cache (kDest 1: 16-byte chunks; 2: bytes)
-    uint4* rows16 = reinterpret_cast<uint4*>(is_v ? p.v_cache : p.k_cache) + head * kChunks;
-    uint8_t* data = (is_v ? p.q4.v_data : p.q4.k_data) + head * q4::kRowBytes;
-    uint8_t* scales = (is_v ? p.q4.v_scales : p.q4.k_scales) + head * q4::kRowScales;
-    const float inv = is_v ? p.q4.v_inv : p.q4.k_inv;
-    uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
-    if (real) {
-      n0 = src[c0];
-      n1 = src[c1];
-    }
-    for (int t = t_begin; t < t_end; ++t) {
-      uint4 a0 = n0, a1 = n1;
-      src += step;
-      if (real && t + 1 < t_end) {
-        n0 = src[c0];
-        n1 = src[c1];
-      }
-      if (!is_v) {
-        float2 x[8];
-        q4::unpack8(a0, x);
-        q4::unpack8(a1, x + 4);
-        if (norm) {
-          float2 ss = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = ffma2(x[i], x[i], ss);
-          float sum = ss.x + ss.y;
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-          const float2 r = both(rsqrtf(sum * (1.f / kHeadDim) + p.eps));
-          float2 w[4];
-          read8(weight + 8 * c0, w);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = fmul2(fmul2(x[i], r), w[i]);
-          read8(weight + 8 * c1, w);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i + 4] = fmul2(fmul2(x[i + 4], r), w[i]);
-        }
-        // The lane's pairs: elements of chunk c0 with those of c1 (halves), or
-        // neighbours within each chunk (interleaved: pairs 4 c0 .., 4 c1 ..).
-        float2 c[4], s[4];
-        if (kInter) {
-          read4(&s_cos[t][4 * c0], c);
-          read4(&s_cos[t][4 * c1], c + 2);
-          read4(&s_sin[t][4 * c0], s);
-          read4(&s_sin[t][4 * c1], s + 2);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float ce = e & 1 ? c[e >> 1].y : c[e >> 1].x, se = e & 1 ? s[e >> 1].y : s[e >> 1].x;
-            const float2 z = x[e];
-            x[e] = make_float2(fmaf(-z.y, se, z.x * ce), fmaf(z.x, se, z.y * ce));
-          }
-        } else {
-          read8(&s_cos[t][8 * l], c);
-          read8(&s_sin[t][8 * l], s);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 v = x[e], z = x[e + 4];
-            x[e] = ffma2(z, make_float2(-s[e].x, -s[e].y), fmul2(v, c[e]));
-            x[e + 4] = ffma2(v, s[e], fmul2(z, c[e]));
-          }
-        }
-        a0 = pack8(x);
-        a1 = pack8(x + 4);
-      }
-      if (!to_cache) {
-        if (real) {
-          out[c0] = a0;
-          out[c1] = a1;
-        }
-        out += out_step;
-      } else if (const int slot = s_slot[t]; slot >= 0) {  // the whole warp
-        const int64_t row = static_cast<int64_t>(slot) * p.num_kv_heads;
-        if (kDest == 1) {
-          if (real) {
-            uint4* dst = rows16 + row * kChunks;
-            dst[c0] = a0;
-            dst[c1] = a1;
-          }
-        } else {
-          uint32_t b0, b1;
-          const uint32_t w0 = q4::quantise_chunk(a0, inv, &b0), w1 = q4::quantise_chunk(a1, inv, &b1);
-          if (real) {
-            uint32_t* d = reinterpret_cast<uint32_t*>(data + row * q4::kRowBytes);
-            d[c0] = w0;
-            d[c1] = w1;
-            if (!(lane & 1)) {  // even chunks: the scale of a group of two
-              uint8_t* sc = scales + row * q4::kRowScales;
-              sc[c0 >> 1] = static_cast<uint8_t>(b0);
-              sc[c1 >> 1] = static_cast<uint8_t>(b1);
-            }
-          }
-        }
-      }
-    }
+    if (g < q_groups)
+      run_group<kDest, kInter, kQ>(p, sh, t0, t_begin, t_end, g, c0, c1);
+    else if (kDest == 0 || g < rope_groups)
+      run_group<kDest, kInter, kK>(p, sh, t0, t_begin, t_end, g - q_groups, c0, c1);
+    else
+      run_group<kDest, kInter, kV>(p, sh, t0, t_begin, t_end, g - rope_groups, c0, c1);
   }
 }
 
