@@ -198,14 +198,16 @@ __device__ __forceinline__ int load_block(const Params& p, int b, int lb) {
   return phys;
 }
 
-// Issue every stage of unit (b, [lo, hi)), lo a multiple of 32, and empty ones up
-// to a multiple of R stages.  Lane 0 of the producer warp only.
+// Issue every stage of unit (b, [lo, hi)), lo a multiple of 32, and empty ones
+// where it has fewer than R.  A head's warps take the stages in turn from one unit
+// into the next, so each has one of the first R and one of the last R.  Lane 0 of
+// the producer warp only.
 template <bool kRows>
 __device__ void emit_unit(const Params& p, const Smem& sm, const CUtensorMap* kmap, const CUtensorMap* vmap,
                           ProducerState& ps, int b, int lo, int hi, int L, int first_phys) {
   int lb_cur = -1, phys = 0, nxt = first_phys;
   const int tile = kStepTokens << p.log2_r;
-  const int end = lo + ((hi - lo + tile - 1) & ~(tile - 1));
+  const int end = lo + max((hi - lo + kStepTokens - 1) & ~(kStepTokens - 1), tile);
   for (int t = lo; t < end; t += kStepTokens) {
     const uint32_t st = ps.stage;
     if (!mbar_wait(&sm.empty[st], ps.phase ^ 1u, &g_err_decode_q4)) {
