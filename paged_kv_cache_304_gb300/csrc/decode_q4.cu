@@ -754,8 +754,6 @@ __global__ void __launch_bounds__(threads_of<NT>(), 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
   const Smem sm = carve(base, p, NT);
   const int warp = threadIdx.x >> 5, R = 1 << p.log2_r;
-  griddep_wait();
-  griddep_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&sm.full[s], 1);
@@ -772,6 +770,8 @@ __global__ void __launch_bounds__(threads_of<NT>(), 1)
     fence_barrier_init();
   }
   __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
   using S = Shape<NT>;
   if (warp >= S::kConsumers) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsProducer));
