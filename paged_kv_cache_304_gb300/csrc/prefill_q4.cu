@@ -166,61 +166,77 @@ __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p_tmem, uint64_t v
 }
 
 // ------------------------------------------------------------------ dequantisation
+// A warp expands 32 tokens.  Codes are loaded four lanes a row, so that a load
+// takes whole rows (a lane a row touched 32 lines with every load; the L1's
+// lookups and half-used sectors then were the expansion's limit): lane l holds
+// 16-byte piece l & 3 (groups 2 (l & 3), + 1) of rows 8 k + l / 4.  Scales are loaded
+// a lane a row.
 struct Packed {
-  uint4 d[4];  // 64 bytes of codes
-  uint2 s;     // 8 scales
+  uint4 d[4];  // codes of rows 8 k + lane / 4
+  uint2 s;     // 8 scales of the lane's own row
+  uint2 vs;    // K: 8 scales of the same token's V row
 };
 
 // L2 prefetch of token `i`'s row of 128-token tile j (its codes and scales).
-__device__ __forceinline__ void prefetch_row(const Params& p, const int32_t* table, int j, bool is_v, int i, int g) {
-  const int phys = __ldg(table + (j >> 1));
+__device__ __forceinline__ void prefetch_row(const Params& p, int phys, int j, bool is_v, int i, int g) {
   if (phys < 0 || phys >= p.c.num_blocks) return;
   const int64_t row = (static_cast<int64_t>(phys) * kBlockSize + (j & 1) * kTileN + i) * p.Hkv + g;
   asm volatile("prefetch.global.L2 [%0];" ::"l"((is_v ? p.c.v_data : p.c.k_data) + row * q4::kRowBytes));
   asm volatile("prefetch.global.L2 [%0];" ::"l"((is_v ? p.c.v_scales : p.c.k_scales) + row * q4::kRowScales));
 }
 
-// Token `i` of 128-token tile j of K or V, kv head g.
-__device__ __forceinline__ void fetch(const Params& p, const int32_t* table, int j, bool is_v, int i, int g, int len,
-                                      Packed& o) {
-  int phys = __ldg(table + (j >> 1));
+// The warp's tokens i0 .. i0 + 31 of 128-token tile j of K or V, kv head g.
+__device__ __forceinline__ void fetch(const Params& p, int phys, int j, bool is_v, int i0, int g, Packed& o) {
   if (phys < 0 || phys >= p.c.num_blocks) {
     atomicOr(&g_err_prefill_q4, PKV_DEVERR_BLOCK_RANGE);
     phys = 0;
   }
-  const int64_t row = (static_cast<int64_t>(phys) * kBlockSize + (j & 1) * kTileN + i) * p.Hkv + g;
-  const uint4* d = reinterpret_cast<const uint4*>((is_v ? p.c.v_data : p.c.k_data) + row * q4::kRowBytes);
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (static_cast<int64_t>(phys) * kBlockSize + (j & 1) * kTileN + i0) * p.Hkv + g;
+  const uint4* d = reinterpret_cast<const uint4*>((is_v ? p.c.v_data : p.c.k_data) + row * q4::kRowBytes) +
+                   ((lane >> 2) * p.Hkv * 4 + (lane & 3));
 #pragma unroll
-  for (int u = 0; u < 4; ++u) o.d[u] = __ldg(d + u);
-  const uint2 vs = __ldg(reinterpret_cast<const uint2*>(p.c.v_scales + row * q4::kRowScales));
-  const uint32_t n0 = q4::nan_bytes(vs.x), n1 = q4::nan_bytes(vs.y);
-  if (is_v) {
-    const bool real = kTileN * j + i < len;
-    o.s = make_uint2(real ? vs.x & ~n0 : 0u, real ? vs.y & ~n1 : 0u);
-  } else {
-    o.s = __ldg(reinterpret_cast<const uint2*>(p.c.k_scales + row * q4::kRowScales));
-    if (n0 | n1) o.s = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-  }
+  for (int k = 0; k < 4; ++k) o.d[k] = __ldg(d + k * (8 * 4) * p.Hkv);
+  const int64_t at = row + lane * p.Hkv;
+  o.s = __ldg(reinterpret_cast<const uint2*>((is_v ? p.c.v_scales : p.c.k_scales) + at * q4::kRowScales));
+  if (!is_v) o.vs = __ldg(reinterpret_cast<const uint2*>(p.c.v_scales + at * q4::kRowScales));
 }
 
-// Its 128 dims into row i of the tile at shared address `dst`.
-__device__ __forceinline__ void expand(const Packed& x, uint32_t dst, int i) {
-  const uint32_t row = dst + i * 128;
+// The lane's row's scales as they are used (apart from the loads, so that nothing
+// waits for them before it must): of a V row zeros in place of NaN and behind the
+// sequence's end, of a K row NaN where the V row holds one.
+__device__ __forceinline__ void settle(Packed& o, bool is_v, bool real) {
+  const uint2 vs = is_v ? o.s : o.vs;
+  const uint32_t n0 = q4::nan_bytes(vs.x), n1 = q4::nan_bytes(vs.y);
+  if (is_v)
+    o.s = make_uint2(real ? vs.x & ~n0 : 0u, real ? vs.y & ~n1 : 0u);
+  else if (n0 | n1)
+    o.s = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
+// The warp's 32 rows of 128 dims into the tile at shared address `dst`.  Lanes 2 and
+// 3 of a row take their piece's halves in the other order: then the eight lanes of
+// a store's phase (two rows) fall into different banks under the swizzle.
+__device__ __forceinline__ void expand(const Packed& x, uint32_t dst, int i0) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+  const bool turned = q >= 2;
+  // 16-byte chunk 4 q + v of row r: 64-dim half q / 2, chunk (4 (q & 1) + v) ^ r in it
+  const uint32_t base = dst + (i0 + r) * 128 + (turned ? kHalfBytes : 0u);
+  const uint32_t x0 = static_cast<uint32_t>(((4 * (q & 1)) | (turned ? 2 : 0)) ^ r) << 4;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    // scales of groups 2u, 2u + 1
-    const uint32_t two = (u < 2 ? x.s.x : x.s.y) >> (16 * (u & 1));
-    const uint32_t f = q4::dec_scale2(two & 0xffffu);
-    const uint32_t f0 = __byte_perm(f, 0, 0x1010), f1 = __byte_perm(f, 0, 0x3232);
-    const uint32_t w[4] = {x.d[u].x, x.d[u].y, x.d[u].z, x.d[u].w};
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t sx = __shfl_sync(0xffffffffu, x.s.x, 8 * k + r), sy = __shfl_sync(0xffffffffu, x.s.y, 8 * k + r);
+    const uint32_t f = q4::dec_scale2(((turned ? sy : sx) >> (16 * (q & 1))) & 0xffffu);
+    const uint32_t f0 = __byte_perm(f, 0, turned ? 0x3232 : 0x1010), f1 = __byte_perm(f, 0, turned ? 0x1010 : 0x3232);
+    const uint4 c = x.d[k];
+    const uint32_t w[4] = {turned ? c.z : c.x, turned ? c.w : c.y, turned ? c.x : c.z, turned ? c.y : c.w};
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       uint32_t o[4];
       q4::dec8(w[v], o);
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = q4::hmul2(o[e], v < 2 ? f0 : f1);
-      const int chunk = 4 * u + v;  // 8 dims
-      const uint32_t a = row + (chunk >> 3) * kHalfBytes + (((chunk & 7) ^ (i & 7)) << 4);
+      const uint32_t a = base + k * 1024 + (x0 ^ (v << 4));
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                    : "memory");
     }
@@ -333,13 +349,14 @@ template <Kinds kinds>
 __device__ __forceinline__ void dequantise(const Params& p, const Smem& sm, const int32_t* table, int j0, int n, int i,
                                            int g, int len) {
   const int lane = threadIdx.x & 31, steps = kinds == kBoth ? 2 * n : n;
-  auto put = [&](int s, const Packed& x) {
+  auto put = [&](int s, Packed& x) {
     int j;
     const bool v = step_of<kinds>(s, n, &j);
     const int st = v ? j % kVStages : j % kKStages;
     const uint32_t par = ((v ? j / kVStages : j / kKStages) & 1) ^ 1;
     if (!mbar_wait(v ? &sm.v_empty[st] : &sm.k_empty[st], par, &g_err_prefill_q4)) return false;
-    expand(x, smem_u32(v ? sm.v0 + st * kTileBytes : sm.k0 + st * kTileBytes), i);
+    settle(x, v, kTileN * (j0 + j) + i < len);
+    expand(x, smem_u32(v ? sm.v0 + st * kTileBytes : sm.k0 + st * kTileBytes), i & ~31);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(v ? &sm.v_full[st] : &sm.k_full[st]);
@@ -347,16 +364,27 @@ __device__ __forceinline__ void dequantise(const Params& p, const Smem& sm, cons
   };
   // Past the end the last step is fetched again: a fetch under a condition would
   // make the registers wait for it where the paths join (15 % on long prompts).
+  // Table entries are loaded a step before they are used.
+  auto entry_of = [&](int s) {
+    int j;
+    step_of<kinds>(min(s, steps - 1), n, &j);
+    return __ldg(table + ((j0 + j) >> 1));
+  };
+  int here, ahead;
   auto get = [&](int s, Packed& x) {
     int j;
     const bool v = step_of<kinds>(min(s, steps - 1), n, &j);
-    fetch(p, table, j0 + j, v, i, g, len, x);
+    fetch(p, here, j0 + j, v, i & ~31, g, x);
+    here = entry_of(s + 1);
     if (kinds != kBoth && s + kAhead < steps) {
       const bool w = step_of<kinds>(s + kAhead, n, &j);
-      prefetch_row(p, table, j0 + j, w, i, g);
+      prefetch_row(p, ahead, j0 + j, w, i, g);
+      ahead = entry_of(s + 1 + kAhead);
     }
   };
   if (n == 0) return;
+  here = entry_of(0);
+  ahead = entry_of(kAhead);
   Packed a, b;
   get(0, a);
   for (int s = 0; s < steps; s += 2) {
@@ -419,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The first rows are on their way into L2 while the barriers and tensor memory
   // are set up.
   const int32_t* table = p.tables + static_cast<int64_t>(seq) * p.maxb;
-  if (nkv > 0 && warp >= 8) prefetch_row(p, table, j0, warp < 12, threadIdx.x & 127, g);
+  if (nkv > 0 && warp >= 8) prefetch_row(p, __ldg(table + (j0 >> 1)), j0, warp < 12, threadIdx.x & 127, g);
   if (threadIdx.x == 0) {
     prefetch_tensormap(&qmap);
     for (int i = 0; i < kKStages; ++i) {
