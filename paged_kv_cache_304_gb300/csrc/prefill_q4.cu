@@ -15,13 +15,13 @@
 //   place, thread r its row r, scaled by a power of two so that the row's largest
 //   element is in [2^14, 2^15); then the softmax, thread r on row r (TMEM lane
 //   r), with the power of two undone in the row's softmax scale.
-// * warps 12-15 (with one slot only, warps 8-11 take the V tiles): thread i turns
-//   token i of the 128-token K and V tiles into fp16: 64 bytes of codes and 8
-//   scales, fetched into registers one step ahead (with one slot, where the loads'
-//   latency shows, also prefetched into L2 six steps ahead; with two, whose K/V
-//   tiles other CTAs read as well, that cost 14 %), become 128 dims (one conversion
-//   and one multiplication per two dims, exact) written in the 128-byte swizzle
-//   that the matrix descriptors expect.
+// * warps 12-15 (with one slot only, warps 8-11 take the V tiles): each
+//   warp turns 32 tokens of the 128-token K and V tiles into fp16: 64 bytes of codes and 8
+//   scales, fetched into registers one step ahead (in split mode with one slot also
+//   prefetched into L2 three steps ahead, 64 -> 61 us on the last 16 tokens of long
+//   prompts; where other CTAs read the same tiles that cost 3 to 14 %), become 128
+//   dims (one conversion and one multiplication per two dims, exact) written in the
+//   128-byte swizzle that the matrix descriptors expect.
 // Tensor memory: S (128 columns, handed from slot to slot), P_A | P_B (64 each,
 // packed fp16), O_A | O_B (128 each); the slots ping-pong so that one slot's
 // products run while the other's softmax does.
@@ -341,11 +341,12 @@ __device__ __forceinline__ bool step_of(int s, int n, int* j) {
   return v;
 }
 
-constexpr int kAhead = 6;  // steps from a row's L2 prefetch to its use
+constexpr int kAhead = 3;  // steps from a row's L2 prefetch to its use
 
 // Expand token `i` of this CTA's n tiles from tile j0 on into the rings, one step
 // fetched into registers while the one before is expanded.
-template <Kinds kinds>
+// kPrefetch: rows are also prefetched into L2, kAhead steps ahead.
+template <Kinds kinds, bool kPrefetch>
 __device__ __forceinline__ void dequantise(const Params& p, const Smem& sm, const int32_t* table, int j0, int n, int i,
                                            int g, int len) {
   const int lane = threadIdx.x & 31, steps = kinds == kBoth ? 2 * n : n;
@@ -370,13 +371,13 @@ __device__ __forceinline__ void dequantise(const Params& p, const Smem& sm, cons
     step_of<kinds>(min(s, steps - 1), n, &j);
     return __ldg(table + ((j0 + j) >> 1));
   };
-  int here, ahead;
+  int here, ahead = 0;
   auto get = [&](int s, Packed& x) {
     int j;
     const bool v = step_of<kinds>(min(s, steps - 1), n, &j);
     fetch(p, here, j0 + j, v, i & ~31, g, x);
     here = entry_of(s + 1);
-    if (kinds != kBoth && s + kAhead < steps) {
+    if (kPrefetch && s + kAhead < steps) {
       const bool w = step_of<kinds>(s + kAhead, n, &j);
       prefetch_row(p, ahead, j0 + j, w, i, g);
       ahead = entry_of(s + 1 + kAhead);
@@ -384,7 +385,7 @@ __device__ __forceinline__ void dequantise(const Params& p, const Smem& sm, cons
   };
   if (n == 0) return;
   here = entry_of(0);
-  ahead = entry_of(kAhead);
+  if (kPrefetch) ahead = entry_of(kAhead);
   Packed a, b;
   get(0, a);
   for (int s = 0; s < steps; s += 2) {
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int slot = warp >= 8 ? 1 : 0;
     if (slot == 1 && !has_b) {
-      dequantise<kValues>(p, sm, table, j0, nkv, threadIdx.x - 256, g, L);
+      dequantise<kValues, kSplit>(p, sm, table, j0, nkv, threadIdx.x - 256, g, L);
     } else {
       // -------------------------------------------------------- softmax + epilogue
       const int wq = warp & 3;
@@ -746,9 +747,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
     if (has_b)
-      dequantise<kBoth>(p, sm, table, j0, nkv, threadIdx.x - 384, g, L);
+      dequantise<kBoth, false>(p, sm, table, j0, nkv, threadIdx.x - 384, g, L);
     else
-      dequantise<kKeys>(p, sm, table, j0, nkv, threadIdx.x - 384, g, L);
+      dequantise<kKeys, kSplit>(p, sm, table, j0, nkv, threadIdx.x - 384, g, L);
   }
   tc::fence_before();
   __syncthreads();
