@@ -445,8 +445,8 @@ PKV_API pkv_status pkv_paged_attn_decode_q4(const pkv_bf16* q, const pkv_q4_cach
  *                 over several CTAs and the pieces joined from there.  The size
  *                 depends on the current device's SM count.
  * A few new tokens per sequence (max_seqlen_q times the query heads of a kv head
- * up to 16, or 32 with many sequences) take the path of decode, with each row's
- * causal limit.
+ * up to 8, 16 or 32, by the number of sequences and max_seqlen_k) take the path of
+ * decode, with each row's causal limit.
  */
 PKV_API size_t pkv_prefill_q4_workspace_bytes(int32_t total_q, int32_t num_seqs, int32_t max_seqlen_q,
                                               int32_t max_seqlen_k, int32_t num_q_heads, int32_t num_kv_heads);

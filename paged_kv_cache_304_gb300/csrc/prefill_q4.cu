@@ -15,9 +15,9 @@
 //   place, thread r its row r, scaled by a power of two so that the row's largest
 //   element is in [2^14, 2^15); then the softmax, thread r on row r (TMEM lane
 //   r), with the power of two undone in the row's softmax scale.
-// * warps 12-15 (with one slot only, warps 8-11 take the V tiles): each
-//   warp turns 32 tokens of the 128-token K and V tiles into fp16: 64 bytes of codes and 8
-//   scales, fetched into registers one step ahead (in split mode with one slot also
+// * warps 12-15 (with one slot only, warps 8-11 take the V tiles): each warp turns
+//   32 tokens of the 128-token K and V tiles into fp16: 64 bytes of codes and 8
+//   scales a token, fetched into registers one step ahead (in split mode with one slot also
 //   prefetched into L2 three steps ahead, 64 -> 61 us on the last 16 tokens of long
 //   prompts; where other CTAs read the same tiles that cost 3 to 14 %), become 128
 //   dims (one conversion and one multiplication per two dims, exact) written in the
@@ -800,6 +800,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t{255}; }
 // How a call is laid out, from sizes that the host knows.
 struct Plan {
   int log2_heads, groups, npairs, tiles;
+  bool fills;  // the query tiles fill the GPU
   int pieces;  // 0: one CTA per query tile; else split mode, the most pieces of a query tile
 };
 
@@ -817,21 +818,23 @@ Plan plan_for(int num_seqs, int max_q, int max_k, int hq, int hkv, int num_sms) 
   // pair) than there are query tiles and the contexts are long enough.
   const int64_t tiles = static_cast<int64_t>(num_seqs) * a.tiles;
   const int budget = num_sms / (hkv * a.npairs);
+  a.fills = tiles >= budget;
   a.pieces = 0;
-  if (tiles > 0 && tiles < budget && tiles <= kMaxSplitTiles && max_k >= 2 * kMinPiece * kTileN)
+  if (tiles > 0 && !a.fills && tiles <= kMaxSplitTiles && max_k >= 2 * kMinPiece * kTileN)
     a.pieces = std::min(budget, ((max_k + kTileN - 1) / kTileN + kMinPiece - 1) / kMinPiece);
   return a;
 }
 
-// Few query rows a kv head go to the streaming kernel: up to 16 always, up to 32
-// when the tile kernel could not split the keys.  Measured (us, streaming / tile
-// kernel; 16 q, 8 kv heads): 4 sequences of 8192-32768 keys with 2, 8, 16 new
-// tokens 34 / 65, 45 / 72, 69 / 72; 4 of 600-1000 keys 12 / 15, -, 27 / 17;
-// 64 of 600-1000 keys 28 / 67, -, 57 / 64; 32 of 8192-32768 keys -, 199 / 561,
-// 386 / 640.
-bool use_rows(const Plan& a, int max_q, int hq, int hkv) {
+// Few query rows a kv head go to the streaming kernel: up to 8 always, up to 16 of
+// long contexts or when the query tiles fill the GPU, up to 32 with both.  Measured
+// (us, streaming / tile kernel; 16 q, 8 kv heads) with 2, 8, 16 new tokens (4, 16, 32
+// rows): 4 sequences of 8192-32768 keys 34 / 56, 45 / 62, 70 / 61; 4 of 600-1000 keys
+// 12 / 14, 17 / 14, 27 / 15; 64 of 600-1000 keys 28 / 59, 37 / 57, 57 / 56; 32 of
+// 8192-32768 keys -, 201 / 492, 388 / 555.
+bool use_rows(const Plan& a, int max_q, int max_k, int hq, int hkv) {
   const int64_t columns = static_cast<int64_t>(max_q) * ((hq + hkv - 1) / hkv);
-  return columns <= 16 || (columns <= 32 && !a.pieces);
+  const bool long_keys = max_k >= 4096;
+  return columns <= 8 || (columns <= 16 && (long_keys || a.fills)) || (columns <= 32 && long_keys && a.fills);
 }
 
 struct WsLayout {
@@ -852,14 +855,14 @@ WsLayout ws_layout(const Plan& a, int num_seqs, int total_q, int hq) {
 size_t prefill_q4_workspace_bytes(int total_q, int num_seqs, int max_seqlen_q, int max_seqlen_k, int num_q_heads,
                                   int num_kv_heads, int num_sms) {
   const Plan a = plan_for(num_seqs, max_seqlen_q, max_seqlen_k, num_q_heads, num_kv_heads, num_sms);
-  if (use_rows(a, max_seqlen_q, num_q_heads, num_kv_heads))
+  if (use_rows(a, max_seqlen_q, max_seqlen_k, num_q_heads, num_kv_heads))
     return rows_q4_workspace_bytes(num_seqs, max_seqlen_q, num_q_heads, num_sms);
   return a.pieces ? ws_layout(a, num_seqs, total_q, num_q_heads).total : 256;
 }
 
 cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
   const Plan pl = plan_for(a.num_seqs, a.max_seqlen_q, a.max_seqlen_k, a.num_q_heads, a.cache.num_kv_heads, num_sms);
-  if (use_rows(pl, a.max_seqlen_q, a.num_q_heads, a.cache.num_kv_heads)) return launch_rows_q4(a, num_sms, stream);
+  if (use_rows(pl, a.max_seqlen_q, a.max_seqlen_k, a.num_q_heads, a.cache.num_kv_heads)) return launch_rows_q4(a, num_sms, stream);
   void (*kernel)(CUtensorMap, Params) = pl.pieces ? prefill_q4_kernel<true> : prefill_q4_kernel<false>;
   // The warpgroups' requests for registers can only be met if the kernel was
   // built with exactly the launch's share per thread.
