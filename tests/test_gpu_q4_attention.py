@@ -227,6 +227,14 @@ def test_prefill_few_rows_at_every_offset(rows, hq, hkv):
     prefill_case([(5000 + rows, 5000)], hq, hkv, seed=rows + 1)
 
 
+@pytest.mark.parametrize("rows,hq,hkv", [(16, 4, 2), (2, 16, 1), (7, 8, 2), (10, 3, 1)])
+def test_prefill_few_rows_of_many_long_sequences(rows, hq, hkv):
+    """As many sequences as fill the GPU, long ones among them: the widest form of the streaming kernel."""
+    lens = (rows, rows + 1, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300, 511, 640)
+    lens = [n + 4200 * (i % 40 == 7) for i, n in enumerate((lens * 12)[:160 // hkv])]
+    prefill_case([(n, n - rows) for n in lens], hq, hkv, seed=rows, ts=(0.37, 1.9), tail=2)
+
+
 @pytest.mark.parametrize("new,cached", [(3, 300), (40, 300), (140, 0), (200, 900)])
 @pytest.mark.parametrize("kv", [0, 1])
 def test_prefill_nan_reaches_only_queries_that_see_it(new, cached, kv):
