@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         const int ch = lane & 15;
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int tr = 32 * wq + 2 * i + (lane >> 4);  // tile row written by this lane
           const int tt = tok0 + (tr >> p.log2_heads);
