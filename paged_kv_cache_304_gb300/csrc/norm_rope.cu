@@ -58,9 +58,17 @@ __device__ __forceinline__ void read4(const float* p, float2* x) {
   x[0] = make_float2(a.x, a.y);
   x[1] = make_float2(a.z, a.w);
 }
-__device__ __forceinline__ void read8(const float* p, float2* x) {
-  read4(p, x);
-  read4(p + 4, x + 2);
+// Eight consecutive values of an array of n that is kept as the first four of every
+// eight and then the other four: eight lanes' reads then take 128 bytes on end and
+// fall into different banks.
+template <int n>
+__device__ __forceinline__ constexpr int place8(int i) {
+  return (i >> 2 & 1) * (n / 2) + (i >> 3) * 4 + (i & 3);
+}
+template <int n>
+__device__ __forceinline__ void read8(const float* p, int i, float2* x) {
+  read4(p + place8<n>(i), x);
+  read4(p + place8<n>(i) + n / 2, x + 2);
 }
 
 // kDest: 0 = k_out, 1 = bf16 cache (K and V), 2 = 4-bit cache (K and V).
@@ -121,10 +129,10 @@ __device__ __forceinline__ void run_group(const NormRopeArgs& p, const Shared& s
         sum += __shfl_xor_sync(0xffffffffu, sum, 4);
         const float2 r = both(rsqrtf(sum * (1.f / kHeadDim) + p.eps));
         float2 w[4];
-        read8(weight + 8 * c0, w);
+        read8<kHeadDim>(weight, 8 * c0, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = fmul2(fmul2(x[i], r), w[i]);
-        read8(weight + 8 * c1, w);
+        read8<kHeadDim>(weight, 8 * c1, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i + 4] = fmul2(fmul2(x[i + 4], r), w[i]);
       }
@@ -143,8 +151,8 @@ __device__ __forceinline__ void run_group(const NormRopeArgs& p, const Shared& s
           x[e] = make_float2(fmaf(-z.y, se, z.x * ce), fmaf(z.x, se, z.y * ce));
         }
       } else {
-        read8(&sh.cos[t][8 * l], c);
-        read8(&sh.sin[t][8 * l], s);
+        read8<kPairs>(sh.cos[t], 8 * l, c);
+        read8<kPairs>(sh.sin[t], 8 * l, s);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 v = x[e], z = x[e + 4];
@@ -238,13 +246,14 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
         s = -s;
       }
     }
-    sh.cos[tok][pair] = c;
-    sh.sin[tok][pair] = s;
+    const int at = kInter ? pair : place8<kPairs>(pair);  // interleaved pairs are read four at a time
+    sh.cos[tok][at] = c;
+    sh.sin[tok][at] = s;
   }
   {
     const uint16_t* w = threadIdx.x < kHeadDim ? p.q_weight : p.k_weight;
     const int d = threadIdx.x % kHeadDim;
-    sh.weight[threadIdx.x / kHeadDim][d] = w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + d)) << 16) : 1.f;
+    sh.weight[threadIdx.x / kHeadDim][place8<kHeadDim>(d)] = w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + d)) << 16) : 1.f;
   }
   if (kDest && threadIdx.x < n) {
     int s = __ldg(p.slots + t0 + threadIdx.x);
