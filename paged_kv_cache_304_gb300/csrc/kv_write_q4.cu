@@ -5,7 +5,7 @@
 // token; a lane owns chunks of 8 dims, so that 32 lanes read 512 contiguous bytes
 // and write 128, and a group of 16 is a pair of lanes that exchange their maxima.
 // All of a token's chunks (up to four of K and four of V per lane) are requested
-// before the first is used.  32768 tokens of 8 kv heads, write and read: 59.6 us,
+// before the first is used.  32768 tokens of 8 kv heads, write and read: 59.5 us,
 // 5.8 TB/s, 86 % of the copy rate (a lane a group of 16, which leaves half-filled
 // sectors: 90 us); the write alone keeps the issue slots 63 % busy.
 #include <cuda_runtime.h>

@@ -34,10 +34,9 @@
 // which ceil(tiles / C) pieces of every query tile need no more CTAs than there
 // are, and takes its piece.  Pieces leave (max, sum, unnormalised output) triples
 // for a combine kernel.
-// Measured: two prompts of 8192 tokens, 32 q and 8 kv heads, 820 us, 1335 TFLOP/s
-// (69 % of the bf16 burst rate; without the expansion's arithmetic no faster); 16384
-// new tokens of ragged prompts of 100 to 1024, 16 q and 8 kv heads, 105 us, of which
-// each query tile's start and end are half.
+// Measured: two prompts of 8192 tokens, 32 q and 8 kv heads, 744 us, 1478 TFLOP/s
+// (76 % of the bf16 burst rate); 16384 new tokens of ragged prompts of 100 to 1024,
+// 16 q and 8 kv heads, 99.5 us, of which each query tile's start and end are half.
 // Every wait is bounded (two seconds); on timeout the CTA flags
 // PKV_DEVERR_WAIT_TIMEOUT, lets the copies and MMAs it has already issued
 // complete, frees its tensor memory and returns.
