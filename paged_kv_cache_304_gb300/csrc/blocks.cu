@@ -242,32 +242,33 @@ __global__ void __launch_bounds__(256) compact_tables_kernel(const CompactArgs p
   }
 }
 
-// One CTA moves one 32 KiB piece at a time; each thread has eight 16-byte loads
-// in flight before its stores.  The same piece of all copies comes before the next
-// piece, so that a block copied to several children is read from HBM once (24
-// children of 16 parents, 28 layers, 1.03 GB: 177.5 us, 5.8 TB/s; copy by copy
-// 214 us.  160 moves in 4 layers, 1.34 GB: 214 us, 6.27 TB/s).
+// A CTA moves 32 KiB pieces of one copy, each thread with eight 16-byte loads in
+// flight before its stores.  Blocks of the grid are ordered copies first, pieces
+// then, so that the same piece of a block copied to several children is read from
+// HBM once, and there are as many as pieces up to kMostCtas: many short CTAs keep the
+// loads and stores of the whole GPU in that order better than a few that loop.  24
+// children of 16 parents, 28 layers, 1.03 GB: 156 us, 6.6 TB/s (1216 CTAs that loop
+// 178 to 186, copy by copy 214); 160 moves in 4 layers, 1.34 GB: 198 us, 6.8 TB/s
+// (214).  Pairs of -1 cost their CTAs a look.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;
+constexpr int64_t kMostCtas = 160000;
 constexpr int64_t kPieceVecs = static_cast<int64_t>(kCopyThreads) * kCopyUnroll;
 
 __global__ void __launch_bounds__(kCopyThreads)
     copy_kernel(uint4* cache, int num_planes, int64_t plane_vecs, int num_blocks, int64_t block_vecs,
-                const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int num_copies) {
+                const int32_t* __restrict__ src, const int32_t* __restrict__ dst) {
   griddep_wait();
   griddep_launch_dependents();
+  const int from = __ldg(src + blockIdx.x), to = __ldg(dst + blockIdx.x);
+  if (from < 0 || to < 0 || from >= num_blocks || to >= num_blocks) {
+    if (!(from == -1 && to == -1) && threadIdx.x == 0) atomicOr(&g_err_blocks, PKV_DEVERR_BLOCK_RANGE);
+    return;
+  }
+  if (from == to) return;
   const int64_t pieces = (block_vecs + kPieceVecs - 1) / kPieceVecs;
-  const int64_t items = pieces * num_planes * num_copies;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t rest = it / num_copies;
-    const int i = static_cast<int>(it - rest * num_copies);
-    const int64_t plane = rest / pieces, piece = rest - plane * pieces;
-    const int from = __ldg(src + i), to = __ldg(dst + i);
-    if (from < 0 || to < 0 || from >= num_blocks || to >= num_blocks) {
-      if (!(from == -1 && to == -1) && threadIdx.x == 0) atomicOr(&g_err_blocks, PKV_DEVERR_BLOCK_RANGE);
-      continue;
-    }
-    if (from == to) continue;
+  for (int64_t it = blockIdx.y; it < pieces * num_planes; it += gridDim.y) {
+    const int64_t plane = it / pieces, piece = it - plane * pieces;
     const uint4* s = cache + plane * plane_vecs + from * block_vecs;
     uint4* d = cache + plane * plane_vecs + to * block_vecs;
     const int64_t v0 = piece * kPieceVecs + threadIdx.x;
@@ -309,12 +310,13 @@ cudaError_t launch_compact_blocks(const CompactArgs& a, int num_sms, cudaStream_
 
 cudaError_t launch_copy_blocks(void* cache, int32_t num_planes, int64_t plane_stride, int32_t num_blocks,
                                int64_t block_bytes, const int32_t* src, const int32_t* dst, int32_t num_copies,
-                               int num_sms, cudaStream_t stream) {
+                               cudaStream_t stream) {
   const int64_t vecs = block_bytes / 16;
-  const int64_t items = (vecs + kPieceVecs - 1) / kPieceVecs * num_planes * num_copies;
-  const int64_t blocks = std::min<int64_t>(items, static_cast<int64_t>(num_sms) * 8);
-  return launch_pdl(copy_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kCopyThreads), 0, stream,
-                    static_cast<uint4*>(cache), num_planes, plane_stride / 16, num_blocks, vecs, src, dst, num_copies);
+  const int64_t items = (vecs + kPieceVecs - 1) / kPieceVecs * num_planes;  // of a copy
+  const int64_t rows = std::min<int64_t>({items, std::max<int64_t>(1, kMostCtas / num_copies), 65535});
+  return launch_pdl(copy_kernel, dim3(static_cast<unsigned>(num_copies), static_cast<unsigned>(rows)),
+                    dim3(kCopyThreads), 0, stream, static_cast<uint4*>(cache), num_planes, plane_stride / 16,
+                    num_blocks, vecs, src, dst);
 }
 
 PKV_DEFINE_READ_ERROR(read_error_blocks, g_err_blocks)

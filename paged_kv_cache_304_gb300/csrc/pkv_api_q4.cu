@@ -396,10 +396,8 @@ pkv_status pkv_copy_blocks(void* cache, int32_t num_planes, int64_t plane_stride
   if (num_planes == 0 || num_copies == 0) return PKV_OK;
   if (!cache || !src || !dst) return PKV_ERR_NULL;
   if (!aligned16(cache)) return PKV_ERR_ALIGN;
-  const int sms = sm_count();
-  if (sms <= 0) return PKV_ERR_CUDA;
   return status_of(launch_copy_blocks(cache, num_planes, plane_stride_bytes, num_blocks, block_bytes, src, dst,
-                                      num_copies, sms, static_cast<cudaStream_t>(stream)));
+                                      num_copies, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -279,7 +279,7 @@ struct CompactArgs {
 cudaError_t launch_compact_blocks(const CompactArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_copy_blocks(void* cache, int32_t num_planes, int64_t plane_stride, int32_t num_blocks,
                                int64_t block_bytes, const int32_t* src, const int32_t* dst, int32_t num_copies,
-                               int num_sms, cudaStream_t stream);
+                               cudaStream_t stream);
 
 // Defines cudaError_t name(uint32_t* out, bool clear): read, and on request
 // reset, the device error word `word` of a translation unit.
