@@ -28,7 +28,7 @@
 // Measured, 16384 tokens of 16 query and 8 kv heads, norm and rotation of three
 // position axes: into new tensors 36.1 us (5.6 TB/s, 83 % of the copy rate), with
 // the bf16 cache write 46.3 us (5.8 TB/s), with the 4-bit write and its read-back
-// 57.0 us, where quantising adds instructions (issue slots 56 % busy); 256 tokens
+// 56.4 us, where quantising adds instructions (issue slots 56 % busy); 256 tokens
 // 2.9 us, latency.
 #include <cuda_runtime.h>
 
