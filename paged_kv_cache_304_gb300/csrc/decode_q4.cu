@@ -319,9 +319,13 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
 #pragma unroll
       for (int i = 0; i < 7; ++i) len[i] = len[i + 1];
       const int n = (L + up) >> log2_tile;
-      const int incl = warp_incl_scan(n, lane);
+      const int incl = warp_incl_scan(n, lane), all = __shfl_sync(0xffffffffu, incl, 31);
+      if (S + all <= my_lo) {  // these 32 end before this CTA's share
+        S += all;
+        continue;
+      }
       const long long Sb = S + incl - n;
-      if (n > 0 && Sb / per == blockIdx.x)
+      if (n > 0 && Sb >= my_lo && Sb < my_hi)
         p.ws_meta[b] = make_int2(static_cast<int>(Sb / per), static_cast<int>((Sb + n - 1) / per));
       const long long lo = my_lo > Sb ? my_lo : Sb;
       const long long hi = my_hi < Sb + n ? my_hi : Sb + n;
@@ -341,7 +345,7 @@ __device__ void producer(const Params& p, const Smem& sm, const CUtensorMap* kma
         if (lane == 0 && ps.ok) emit_unit<kRows>(p, sm, kmap, vmap, ps, bj, loj, hij, Lj, physj);
         ps.ok = __shfl_sync(0xffffffffu, ps.ok, 0);
       }
-      S += __shfl_sync(0xffffffffu, incl, 31);
+      S += all;
     }
   }
   // One end mark for each of a head's R warps.
