@@ -427,8 +427,8 @@ __device__ void consumer(const Params& p, const Smem& sm) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const int col = min(g + 8 * n, columns - 1), tok = col / p.G;
-          const uint4* row = reinterpret_cast<const uint4*>(
-                                 p.q + (static_cast<int64_t>(q0 + tok) * p.Hq + h * p.G + col - tok * p.G) * kHeadDim) + 4 * c;
+          const int64_t at = static_cast<int64_t>(q0 + tok) * p.Hq + h * p.G + col - tok * p.G;
+          const uint4* row = reinterpret_cast<const uint4*>(p.q + at * kHeadDim) + 4 * c;
 #pragma unroll
           for (int i = 0; i < 4; ++i) raw[kRows ? n : 0][i] = __ldg(row + i);
         }
@@ -436,7 +436,8 @@ __device__ void consumer(const Params& p, const Smem& sm) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const bool real = g + 8 * n < columns;
-        const uint32_t src = smem_u32(sm.qbuf) + qs * p.q_slot_bytes + (h * p.G + (real ? g + 8 * n : 0)) * (kHeadDim * 2) + c * 64;
+        const uint32_t src = smem_u32(sm.qbuf) + qs * p.q_slot_bytes +
+                             (h * p.G + (real ? g + 8 * n : 0)) * (kHeadDim * 2) + c * 64;
         auto load = [&](int i) { return kRows ? raw[kRows ? n : 0][i] : lds128(src + 16 * i); };
         float top = 0.f;
 #pragma unroll
@@ -735,7 +736,8 @@ __device__ void consumer(const Params& p, const Smem& sm) {
               float4* dst = reinterpret_cast<float4*>(p.ws_o + at * kHeadDim + 16 * g);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                dst[i] = make_float4(acc[n][2 * i][k], acc[n][2 * i][k + 2], acc[n][2 * i + 1][k], acc[n][2 * i + 1][k + 2]);
+                dst[i] = make_float4(acc[n][2 * i][k], acc[n][2 * i][k + 2], acc[n][2 * i + 1][k],
+                                     acc[n][2 * i + 1][k + 2]);
               if (g == 0) p.ws_ml[at] = make_float2(m[n][k], l[n][k]);
             }
           }

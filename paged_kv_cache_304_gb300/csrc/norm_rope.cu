@@ -93,7 +93,8 @@ __device__ __forceinline__ void run_group(const NormRopeArgs& p, const Shared& s
   const bool real = head < (is_q ? p.num_q_heads : p.num_kv_heads);
   // Steps and places in 16-byte chunks; plain loads: the output may be the input.
   const int64_t step = (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) >> 3;
-  const uint4* src = reinterpret_cast<const uint4*>(is_q ? p.q : is_v ? p.v : p.k) + (t0 + t_begin) * step + head * kChunks;
+  const uint4* src =
+      reinterpret_cast<const uint4*>(is_q ? p.q : is_v ? p.v : p.k) + (t0 + t_begin) * step + head * kChunks;
   const int64_t out_step = (is_q ? p.q_out_stride : p.k_out_stride) >> 3;
   uint4* out = reinterpret_cast<uint4*>(is_q ? p.q_out : p.k_out) + (t0 + t_begin) * out_step + head * kChunks;
   const bool norm = (is_q ? p.q_weight : p.k_weight) != nullptr;
@@ -253,7 +254,8 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
   {
     const uint16_t* w = threadIdx.x < kHeadDim ? p.q_weight : p.k_weight;
     const int d = threadIdx.x % kHeadDim;
-    sh.weight[threadIdx.x / kHeadDim][place8<kHeadDim>(d)] = w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + d)) << 16) : 1.f;
+    sh.weight[threadIdx.x / kHeadDim][place8<kHeadDim>(d)] =
+        w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + d)) << 16) : 1.f;
   }
   if (kDest && threadIdx.x < n) {
     int s = __ldg(p.slots + t0 + threadIdx.x);
@@ -295,7 +297,9 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, int dest, int num_sms, cudaS
   if (a.interleaved)
     kernel = dest == 0 ? norm_rope_kernel<0, true> : dest == 1 ? norm_rope_kernel<1, true> : norm_rope_kernel<2, true>;
   else
-    kernel = dest == 0 ? norm_rope_kernel<0, false> : dest == 1 ? norm_rope_kernel<1, false> : norm_rope_kernel<2, false>;
+    kernel = dest == 0   ? norm_rope_kernel<0, false>
+             : dest == 1 ? norm_rope_kernel<1, false>
+                         : norm_rope_kernel<2, false>;
   return launch_pdl(kernel, grid, block, 0, stream, a, tokens);
 }
 

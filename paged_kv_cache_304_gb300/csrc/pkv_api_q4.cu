@@ -103,7 +103,8 @@ pkv_status norm_rope_common(const pkv_bf16* q, int64_t q_stride, const pkv_bf16*
   if (!q || !q_out || (num_kv_heads && !k) || (nr->rope_dim && (!nr->freqs || !nr->positions))) return PKV_ERR_NULL;
   if (nr->rope_dim && (reinterpret_cast<uintptr_t>(nr->freqs) & 7u)) return PKV_ERR_ALIGN;
   if (!aligned16(nr->q_weight) || !aligned16(nr->k_weight)) return PKV_ERR_ALIGN;
-  const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_dim, k_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_dim;
+  const int64_t k_row = static_cast<int64_t>(num_kv_heads) * head_dim;
   pkv_status st = check_rows(q, q_stride, q_row);
   if (st == PKV_OK) st = check_rows(q_out, q_out_stride, q_row);
   if (st == PKV_OK && num_kv_heads) st = check_rows(k, k_stride, k_row);

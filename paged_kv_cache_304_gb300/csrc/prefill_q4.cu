@@ -861,7 +861,8 @@ size_t prefill_q4_workspace_bytes(int total_q, int num_seqs, int max_seqlen_q, i
 
 cudaError_t launch_paged_attn_prefill_q4(const AttnQ4Args& a, int num_sms, cudaStream_t stream) {
   const Plan pl = plan_for(a.num_seqs, a.max_seqlen_q, a.max_seqlen_k, a.num_q_heads, a.cache.num_kv_heads, num_sms);
-  if (use_rows(pl, a.max_seqlen_q, a.max_seqlen_k, a.num_q_heads, a.cache.num_kv_heads)) return launch_rows_q4(a, num_sms, stream);
+  if (use_rows(pl, a.max_seqlen_q, a.max_seqlen_k, a.num_q_heads, a.cache.num_kv_heads))
+    return launch_rows_q4(a, num_sms, stream);
   void (*kernel)(CUtensorMap, Params) = pl.pieces ? prefill_q4_kernel<true> : prefill_q4_kernel<false>;
   // The warpgroups' requests for registers can only be met if the kernel was
   // built with exactly the launch's share per thread.
