@@ -433,7 +433,8 @@ PKV_API pkv_status pkv_paged_attn_decode_q4(const pkv_bf16* q, const pkv_q4_cach
 /*
  * Varlen causal prefill over the 4-bit cache: pkv_paged_attn_prefill with K and
  * V the values the cache holds; rounding as in pkv_paged_attn_decode_q4.  A V
- * group that reads as NaN makes all 128 dims of the rows that see its token NaN.
+ * group that reads as NaN makes its 16 dims, and possibly all 128, NaN in the rows
+ * that see its token, and reaches no other row.
  *   max_seqlen_q, max_seqlen_k  upper bounds of n_i and L_i.  A sequence beyond
  *                 them, with c_i < 0 or with L_i > max_blocks_per_seq *
  *                 block_size flags PKV_DEVERR_LEN_RANGE and its rows are not
